@@ -1,7 +1,7 @@
 /*
  * moe_lora.h -- C ABI of the MI355X (gfx950) MoE-LoRA hot path.
  *
- * Two operations, both hand-written HIP kernels:
+ * The two operations of the adapters, both hand-written HIP kernels:
  *
  *   moe_lora_align  -- per LoRA slot, group the routed (token, k) pairs by
  *                      expert and pad every group to block_m (vLLM PR #29257
@@ -11,6 +11,10 @@
  *                      rank-r vector kept on chip, optional routed weight
  *                      (prhub summary of vLLM PR #42290, implementation
  *                      steps and key source fragment).
+ *
+ * and, further down, the 8-bit base side they stand beside: rows of e4m3
+ * values from an RMS norm or a gated activation, and the e4m3 product, dense
+ * or over the align step's blocks.
  *
  * Conventions for every call below:
  *   - Pointers marked [device] are device (HBM) addresses; the caller owns
@@ -414,6 +418,102 @@ MOE_LORA_API int fused_moe_lora_two_kernel(const uint16_t *x, int32_t x_per_pair
  */
 MOE_LORA_API int moe_lora_accumulate(uint16_t *y, const uint16_t *delta, int64_t n,
                    void *stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit base side of a layer: norm -> w13 -> (adapters) -> activation ->
+ * w2 -> (adapters).  The pages' base fused-MoE GEMM has an 8-bit form that
+ * consumes the same align outputs as the adapters (prhub summary of vLLM PR
+ * #42290, the TritonExperts fragment).
+ *
+ * 8-bit rows are OCP e4m3 values q [M, K] with fp32 scales
+ * [ceil(K / 128), M]: one scale per row and block of 128 columns (the last
+ * block may be shorter), block-major, because the product reads one block of
+ * many rows at a time.  A value is q * scale.  The producers take
+ *     scale = max(2^-40, largest magnitude of the block) / 448,
+ *     q     = e4m3(value / scale), to nearest, ties to even;
+ * NaN entries are passed over by the maximum and are NaN in q; an infinity
+ * makes its block's scale infinite and is NaN in q, so either reaches the
+ * row's products as NaN.
+ * ------------------------------------------------------------------------ */
+
+/* Columns that share a scale; widest row of moe_lora_rms_norm_fp8. */
+#define MOE_LORA_FP8_BLOCK 128
+#define MOE_LORA_RMS_NORM_MAX_WIDTH 65536
+
+/*
+ * moe_lora_rms_norm_fp8 -- for every row of x:
+ *     h = bf16(x + residual)         (x itself when residual is NULL)
+ *     v = h / sqrt(mean(h^2) + eps) * weight          (fp32)
+ * h goes to residual_out, bf16(v) to y, v to q and scales.
+ * [device] x, residual: bf16 [M, H] (residual may be NULL); weight: bf16 [H];
+ *          residual_out: bf16 [M, H], NULL exactly when residual is; it may be
+ *          residual or x itself; y: bf16 [M, H] or NULL (the rows the adapters
+ *          and the router read); q: e4m3 [M, H]; scales: fp32
+ *          [ceil(H / 128), M].  Otherwise outputs overlap no input.
+ * H a multiple of 8; all but scales 16-byte aligned.  MOE_LORA_ERR_UNSUPPORTED
+ * for H > MOE_LORA_RMS_NORM_MAX_WIDTH or M >= 2^31; MOE_LORA_ERR_INVALID for
+ * eps < 0 or NaN.  M == 0 does nothing.  Deterministic.
+ */
+MOE_LORA_API int moe_lora_rms_norm_fp8(const uint16_t *x, const uint16_t *residual,
+                   const uint16_t *weight, int64_t M, int32_t H, float eps,
+                   uint16_t *residual_out, uint16_t *y, uint8_t *q, float *scales,
+                   void *stream);
+
+/*
+ * moe_lora_silu_mul_fp8 -- v = silu(gate) * up for every row of y = [gate | up]
+ * (the two slices of a w13 projection, silu(g) = g / (1 + exp(-g)), fp32);
+ * bf16(v) to h, v to q and scales: the inputs of the adapters' and the base
+ * side's w2.
+ * [device] y: bf16 [P, 2 I]; h: bf16 [P, I] or NULL; q: e4m3 [P, I]; scales:
+ *          fp32 [ceil(I / 128), P].  Outputs overlap no input.
+ * I a multiple of 8; all but scales 16-byte aligned.  MOE_LORA_ERR_UNSUPPORTED
+ * for P >= 2^31 or I >= 2^30.  P == 0 does nothing.  Deterministic.
+ */
+MOE_LORA_API int moe_lora_silu_mul_fp8(const uint16_t *y, int64_t P, int32_t I, uint16_t *h,
+                   uint8_t *q, float *scales, void *stream);
+
+/*
+ * moe_lora_fp8_gemm -- for every row m, slice s and column n < Ns:
+ *     Y[m, s*Ns+n] = bf16( sum_j x_scales[j, m] * w_scales[s, n/128, j]
+ *                          * sum_{k in block j} x[m, k] * w[s, n, k] )
+ * summed in fp32.
+ * [device] x, x_scales: 8-bit rows [M, K]; w: e4m3 [S, Ns, K]; w_scales: fp32
+ *          [S, ceil(Ns / 128), ceil(K / 128)]; y: bf16 [M, S*Ns], overlapping
+ *          no input.
+ * K a multiple of 16, Ns of 8; x, w and y 16-byte aligned.
+ * MOE_LORA_ERR_UNSUPPORTED when a slice of w has 2^31 elements or more, S*Ns
+ * does, or x_scales exceeds 2 GiB.  M == 0 does nothing.  Deterministic.
+ */
+MOE_LORA_API int moe_lora_fp8_gemm(const uint8_t *x, const float *x_scales, const uint8_t *w,
+                   const float *w_scales, int64_t M, int32_t K, int32_t Ns, int32_t S,
+                   uint16_t *y, void *stream);
+
+/*
+ * moe_lora_fp8_moe_gemm -- the same product for the routed pairs: for every
+ * pair p = m*topk + k in the align outputs (of one slot: moe_lora_align with
+ * L = 1 and a zero mapping), with its block's expert e,
+ *     Y[p, s*Ns+n] = bf16( w[p] * sum_j x_scales[j, row] * w_scales[e, s, n/128, j]
+ *                          * sum_{k in block j} x[row, k] * w[e, s, n, k] ),
+ * row = p if x_per_pair else m, w[p] = topk_weights[p] if mul_routed_weight
+ * else 1.  Rows of pairs in no block are not touched; ids outside their range
+ * are passed over.
+ * [device] x, x_scales: 8-bit rows [M, K] or [M*topk, K]; w: e4m3
+ *          [E, S, Ns, K]; w_scales: fp32 [E, S, ceil(Ns/128), ceil(K/128)];
+ *          sorted_token_ids [cap], expert_ids [cap / block_m],
+ *          num_tokens_post_padded [1]: moe_lora_align's for the same M, topk,
+ *          E, block_m; topk_weights: fp32 [M, topk], may be NULL when
+ *          mul_routed_weight == 0; y: bf16 [M, topk, S*Ns], overlapping no
+ *          input.
+ * Sizes and alignment as moe_lora_align and moe_lora_fp8_gemm;
+ * MOE_LORA_ERR_UNSUPPORTED also when x exceeds 2 GiB.  M == 0 does nothing.
+ * Deterministic.
+ */
+MOE_LORA_API int moe_lora_fp8_moe_gemm(const uint8_t *x, const float *x_scales,
+                   int32_t x_per_pair, const uint8_t *w, const float *w_scales,
+                   const int32_t *sorted_token_ids, const int32_t *expert_ids,
+                   const int32_t *num_tokens_post_padded, const float *topk_weights,
+                   int32_t mul_routed_weight, int64_t M, int32_t topk, int32_t K, int32_t Ns,
+                   int32_t S, int32_t E, int32_t block_m, uint16_t *y, void *stream);
 
 #ifdef __cplusplus
 }

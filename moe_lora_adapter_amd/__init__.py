@@ -8,6 +8,13 @@ raise; there is no fallback implementation.
     out = moe_lora_align(topk_ids, token_lora_mapping, E, L, block_m)
     fused_moe_lora(x, lora_a, lora_b, out, topk_weights, y,
                    mul_routed_weight=..., add_inputs=..., x_per_pair=...)
+
+The 8-bit base side of the same layer:
+
+    x8 = moe_lora_rms_norm_fp8(x, weight, eps=..., residual=..., y=hidden)
+    moe_lora_fp8_moe_gemm(x8, w13, w13_scales, base_align, None, y, ...)
+    h8 = moe_lora_silu_mul_fp8(y, h=h)
+    moe_lora_fp8_moe_gemm(h8, w2, w2_scales, base_align, topk_weights, y2, ...)
 """
 
 from __future__ import annotations
@@ -58,12 +65,20 @@ SIGNATURES = {
                                                  _I32, _I64, _I32, _I32, _I32, _I32, _I32, _I32,
                                                  _I32, _I32, _P, _P, _I64, _P]),
     "moe_lora_accumulate": (ctypes.c_int, [_P, _P, _I64, _P]),
+    "moe_lora_rms_norm_fp8": (ctypes.c_int, [_P, _P, _P, _I64, _I32, ctypes.c_float, _P, _P, _P,
+                                             _P, _P]),
+    "moe_lora_silu_mul_fp8": (ctypes.c_int, [_P, _I64, _I32, _P, _P, _P, _P]),
+    "moe_lora_fp8_gemm": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _P]),
+    "moe_lora_fp8_moe_gemm": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P, _P, _I32, _I64,
+                                             _I32, _I32, _I32, _I32, _I32, _I32, _P, _P]),
 }
 
 NAIVE_MAX_PAIRS = 1024        # MOE_LORA_NAIVE_MAX_PAIRS
 WITH_ALIGN_MAX_PAIRS = 64     # MOE_LORA_WITH_ALIGN_MAX_PAIRS
 WITH_ALIGN_MAX_SLOTS = 64     # MOE_LORA_WITH_ALIGN_MAX_SLOTS
 TWO_KERNEL_MAX_RANK = 512     # MOE_LORA_TWO_KERNEL_MAX_RANK
+FP8_BLOCK = 128               # MOE_LORA_FP8_BLOCK
+RMS_NORM_MAX_WIDTH = 65536    # MOE_LORA_RMS_NORM_MAX_WIDTH
 
 
 class MoeLoraError(RuntimeError):
@@ -411,4 +426,153 @@ def moe_lora_accumulate(y, delta, stream=None):
     rc = lib().moe_lora_accumulate(_dptr(y), _dptr(delta), y.numel(), _stream_ptr(stream))
     if rc != OK:
         raise MoeLoraError(rc, "moe_lora_accumulate")
+    return y
+
+
+@dataclass
+class Fp8Rows:
+    """8-bit rows: a value is q * scale of its row and block of 128 columns."""
+    q: "object"        # float8_e4m3fn [M, K]
+    scales: "object"   # float32 [ceil(K / 128), M]
+
+
+def fp8_blocks(n: int) -> int:
+    """Scale blocks of n columns."""
+    return -(-n // FP8_BLOCK)
+
+
+def alloc_fp8_rows(M: int, K: int, device) -> Fp8Rows:
+    import torch
+    return Fp8Rows(torch.empty((M, K), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty((fp8_blocks(K), M), dtype=torch.float32, device=device))
+
+
+def _check_shape(t, name, dtype, device, shape):
+    """_check with the shape; the message is formed only for a call that is refused."""
+    if (t.__class__.__name__ in ("Tensor", "Parameter") and t.dtype is dtype
+            and tuple(t.shape) == shape and t.is_contiguous() and t.device == device):
+        return
+    _check(t, name, dtype, device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _launch(name, device, stream, *args):
+    """Call an entry point on `device`: its stream last, that device current."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs tensors on a GPU, got {device}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _launch(name, device, stream, *args)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    rc = getattr(lib(), name)(*args, s.cuda_stream)
+    if rc != OK:
+        raise MoeLoraError(rc, name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_lora_rms_norm_fp8(x, weight, *, eps: float = 1e-6, residual=None, residual_out=None, y=None,
+                          out: Fp8Rows | None = None, stream=None) -> Fp8Rows:
+    """RMS norm of x (+ residual) as 8-bit rows, and as bf16 in y when given; the sum goes to
+    residual_out (None: in place on residual); see moe_lora.h."""
+    import torch
+    bf, dev = torch.bfloat16, x.device
+    _check(x, "x", bf, dev)
+    if x.dim() != 2:
+        raise ValueError("x must be [M, H]")
+    M, H = x.shape
+    _check_shape(weight, "weight", bf, dev, (H,))
+    if residual is not None:
+        _check_shape(residual, "residual", bf, dev, (M, H))
+        residual_out = residual if residual_out is None else residual_out
+        _check_shape(residual_out, "residual_out", bf, dev, (M, H))
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if y is not None:
+        _check_shape(y, "y", bf, dev, (M, H))
+    if out is None:
+        out = alloc_fp8_rows(M, H, dev)
+    _check_shape(out.q, "out.q", torch.float8_e4m3fn, dev, (M, H))
+    _check_shape(out.scales, "out.scales", torch.float32, dev, (fp8_blocks(H), M))
+    _launch("moe_lora_rms_norm_fp8", dev, stream, _ptr(x), _ptr(residual), _ptr(weight), M, H, eps,
+            _ptr(residual_out), _ptr(y), _ptr(out.q), _ptr(out.scales))
+    return out
+
+
+def moe_lora_silu_mul_fp8(y, *, h=None, out: Fp8Rows | None = None, stream=None) -> Fp8Rows:
+    """silu(gate) * up of y = [..., gate | up] as 8-bit rows, and as bf16 in h when given; see
+    moe_lora.h."""
+    import torch
+    dev = y.device
+    _check(y, "y", torch.bfloat16, dev)
+    if y.dim() < 2 or y.shape[-1] % 2:
+        raise ValueError("y must be [..., 2 * I]")
+    I = y.shape[-1] // 2
+    P = y.numel() // max(1, 2 * I)
+    if h is not None:
+        _check_shape(h, "h", torch.bfloat16, dev, (P, I))
+    if out is None:
+        out = alloc_fp8_rows(P, I, dev)
+    _check_shape(out.q, "out.q", torch.float8_e4m3fn, dev, (P, I))
+    _check_shape(out.scales, "out.scales", torch.float32, dev, (fp8_blocks(I), P))
+    _launch("moe_lora_silu_mul_fp8", dev, stream, _ptr(y), P, I, _ptr(h), _ptr(out.q),
+            _ptr(out.scales))
+    return out
+
+
+def moe_lora_fp8_gemm(x: Fp8Rows, w, w_scales, y=None, *, stream=None):
+    """8-bit rows times w [S, Ns, K] (e4m3, a scale per 128 x 128 block of a slice); y bf16
+    [M, S*Ns] is allocated when not given; see moe_lora.h."""
+    import torch
+    f8, dev = torch.float8_e4m3fn, w.device
+    _check(w, "w", f8, dev)
+    if w.dim() != 3 or x.q.dim() != 2:
+        raise ValueError("w must be [S, Ns, K] and x.q [M, K]")
+    S, Ns, K = w.shape
+    M = x.q.shape[0]
+    _check_shape(w_scales, "w_scales", torch.float32, dev, (S, fp8_blocks(Ns), fp8_blocks(K)))
+    _check_shape(x.q, "x.q", f8, dev, (M, K))
+    _check_shape(x.scales, "x.scales", torch.float32, dev, (fp8_blocks(K), M))
+    if y is None:
+        y = torch.empty((M, S * Ns), dtype=torch.bfloat16, device=dev)
+    _check_shape(y, "y", torch.bfloat16, dev, (M, S * Ns))
+    _launch("moe_lora_fp8_gemm", dev, stream, _ptr(x.q), _ptr(x.scales), _ptr(w), _ptr(w_scales),
+            M, K, Ns, S, _ptr(y))
+    return y
+
+
+def moe_lora_fp8_moe_gemm(x: Fp8Rows, w, w_scales, align: AlignOutput, topk_weights, y, *,
+                          mul_routed_weight: bool, x_per_pair: bool = False, stream=None):
+    """8-bit rows times each routed pair's expert of w [E, S, Ns, K], into y [M, topk, S*Ns]; align
+    is one slot's (L = 1); see moe_lora.h."""
+    import torch
+    f8, i32, dev = torch.float8_e4m3fn, torch.int32, y.device
+    _check(y, "y", torch.bfloat16, dev)
+    _check(w, "w", f8, dev)
+    if w.dim() != 4 or y.dim() != 3 or x.q.dim() != 2:
+        raise ValueError("w must be [E, S, Ns, K], y [M, topk, S*Ns] and x.q [rows, K]")
+    E, S, Ns, K = w.shape
+    M, topk, N = y.shape
+    if N != S * Ns:
+        raise ValueError("y's last dim must be S*Ns")
+    rows, kb = M * topk if x_per_pair else M, fp8_blocks(K)
+    _check_shape(w_scales, "w_scales", torch.float32, dev, (E, S, fp8_blocks(Ns), kb))
+    _check_shape(x.q, "x.q", f8, dev, (rows, K))
+    _check_shape(x.scales, "x.scales", torch.float32, dev, (kb, rows))
+    if topk_weights is not None:
+        _check_shape(topk_weights, "topk_weights", torch.float32, dev, (M, topk))
+    cap = align_capacity(M, topk, E, align.block_m)
+    _check_shape(align.sorted_token_ids, "align.sorted_token_ids", i32, dev, (1, cap))
+    _check_shape(align.expert_ids, "align.expert_ids", i32, dev, (1, cap // align.block_m))
+    _check_shape(align.num_tokens_post_padded, "align.num_tokens_post_padded", i32, dev, (1,))
+    _launch("moe_lora_fp8_moe_gemm", dev, stream, _ptr(x.q), _ptr(x.scales),
+            int(bool(x_per_pair)), _ptr(w), _ptr(w_scales), _ptr(align.sorted_token_ids),
+            _ptr(align.expert_ids), _ptr(align.num_tokens_post_padded), _ptr(topk_weights),
+            int(bool(mul_routed_weight)), M, topk, K, Ns, S, E, align.block_m, _ptr(y))
     return y

@@ -1,0 +1,182 @@
+// Producers of 8-bit rows: RMS norm with the residual's addition, and
+// silu(gate) * up.  Both are bound by memory: every value is read once, held
+// in registers, and written once in each of the forms a layer reads (the
+// stored residual, bf16 rows for the LoRA side, e4m3 rows for the base
+// product).
+#include <algorithm>
+
+#include "common.h"
+#include "fp8.h"
+#include "internal.h"
+
+namespace mlr {
+namespace {
+
+// Largest of v over the 16 consecutive lanes of a DPP row (one 128-column
+// block at 8 columns a lane), in every one of them.
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, butterfly_partner(v, 8));
+  v = fmaxf(v, butterfly_partner(v, 4));
+  v = fmaxf(v, butterfly_partner(v, 2));
+  v = fmaxf(v, butterfly_partner(v, 1));
+  return v;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+
+// Largest magnitude of 8 values; NaN entries are passed over (fmaxf), so one
+// NaN leaves its block's other values as they are.
+__device__ __forceinline__ float amax8(const float (&f)[8]) {
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(f[i]));
+  return a;
+}
+
+// Scale of a block from its largest magnitude: the division is the IEEE one.
+__device__ __forceinline__ float block_scale(float amax) { return fmaxf(amax, kMinAmax) / kE4m3Max; }
+
+// 8 values over the scale, rounded once to e4m3 (nearest even).  |v| * inv is
+// at most 448 (1 + 2^-22), which rounds to 448: the conversion never overflows
+// on finite values.  An infinite block has inv = 0: its infinities become NaN.
+__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0] * inv, f[1] * inv, 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2] * inv, f[3] * inv, lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4] * inv, f[5] * inv, 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6] * inv, f[7] * inv, hi, true);
+  return make_uint2(uint32_t(lo), uint32_t(hi));
+}
+
+// One workgroup of T threads a row; thread t holds the 8-column chunks t,
+// t + T, ... (CH of them).
+template <int T, int CH, bool RES>
+__global__ void __launch_bounds__(T) rms_norm_fp8_kernel(NormParams p) {
+  __shared__ float part[T / kWave];
+  const int64_t row = blockIdx.x;
+  const int nc = p.H / 8;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.H);
+  float v[CH][8];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + i * T;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (c < nc) {
+      unpack8(x[c], v[i]);
+      if constexpr (RES) {
+        float r[8];
+        unpack8(reinterpret_cast<const uint4*>(p.residual + row * p.H)[c], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+        // the norm is of the sum as it is stored
+        const uint4 h = pack8(v[i]);
+        reinterpret_cast<uint4*>(p.residual_out + row * p.H)[c] = h;
+        unpack8(h, v[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += butterfly_partner(sum, o);
+  if constexpr (T > kWave) {
+    if (lane_id() == 0) part[wave_id()] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < T / kWave; ++i) sum += part[i];
+  }
+  const float rstd = 1.0f / sqrtf(sum / float(p.H) + p.eps);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = threadIdx.x + i * T;
+    float amax = 0.0f;
+    if (c < nc) {
+      float w[8];
+      unpack8(reinterpret_cast<const uint4*>(p.weight)[c], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
+      amax = amax8(v[i]);
+    }
+    const float s = block_scale(row16_max(amax));
+    if (c < nc) {
+      if (p.y) reinterpret_cast<uint4*>(p.y + row * p.H)[c] = pack8(v[i]);
+      reinterpret_cast<uint2*>(p.q + row * p.H)[c] = quantise8(v[i], 1.0f / s);
+      if ((c & 15) == 0) p.scales[int64_t(c >> 4) * p.M + row] = s;
+    }
+  }
+}
+
+// 16 lanes a (row, block of 128 columns).
+constexpr int kTS = 256;
+__global__ void __launch_bounds__(kTS) silu_mul_fp8_kernel(SiluParams p, int32_t nb) {
+  const int64_t items = p.P * nb;
+  const int64_t stride = int64_t(gridDim.x) * (kTS / 16);
+  const int sub = threadIdx.x & 15;
+  for (int64_t it = int64_t(blockIdx.x) * (kTS / 16) + threadIdx.x / 16; it < items; it += stride) {
+    const int64_t row = it / nb;
+    const int j = int(it - row * nb);
+    const int col = j * kScaleBlock + sub * 8;
+    float v[8];
+    float amax = 0.0f;
+    if (col < p.I) {
+      const uint16_t* g = p.y + row * 2 * p.I + col;
+      float u[8];
+      unpack8(*reinterpret_cast<const uint4*>(g), v);
+      unpack8(*reinterpret_cast<const uint4*>(g + p.I), u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] / (1.0f + __expf(-v[i])) * u[i];
+      amax = amax8(v);
+    }
+    const float s = block_scale(row16_max(amax));
+    if (col < p.I) {
+      if (p.h) *reinterpret_cast<uint4*>(p.h + row * p.I + col) = pack8(v);
+      *reinterpret_cast<uint2*>(p.q + row * p.I + col) = quantise8(v, 1.0f / s);
+      if (sub == 0) p.scales[int64_t(j) * p.P + row] = s;
+    }
+  }
+}
+
+template <int T, int CH>
+hipError_t norm_of(const NormParams& p, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(p.M));
+  if (p.residual)
+    hipLaunchKernelGGL((rms_norm_fp8_kernel<T, CH, true>), grid, dim3(T), 0, st, p);
+  else
+    hipLaunchKernelGGL((rms_norm_fp8_kernel<T, CH, false>), grid, dim3(T), 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm_fp8(const NormParams& p, hipStream_t st) {
+  const int nc = p.H / 8;
+  if (nc <= 256) return norm_of<256, 1>(p, st);
+  if (nc <= 512) return norm_of<256, 2>(p, st);
+  if (nc <= 1024) return norm_of<256, 4>(p, st);
+  if (nc <= 2048) return norm_of<1024, 2>(p, st);
+  return norm_of<1024, 8>(p, st);
+}
+
+hipError_t launch_silu_mul_fp8(const SiluParams& p, hipStream_t st) {
+  const int32_t nb = int32_t(scale_blocks(p.I));
+  const int64_t want = (p.P * nb + kTS / 16 - 1) / (kTS / 16);
+  const int64_t cap = int64_t(std::max(xcd_compute_units(), 1)) * kXcds * 16;
+  hipLaunchKernelGGL(silu_mul_fp8_kernel, dim3(unsigned(std::min(want, cap))), dim3(kTS), 0, st, p, nb);
+  return hipGetLastError();
+}
+
+}  // namespace mlr
