@@ -11,6 +11,7 @@ using namespace mlr;
 namespace {
 
 constexpr int64_t kInt32Max = 2147483647;
+constexpr int64_t kMaxK = int64_t(1) << 22;  // a tile of 256 rows stays below 2 GiB
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -19,7 +20,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // scale blocks.
 int check_weights(int64_t K, int64_t Ns, int64_t S, GemmParams* p) {
   if (K < 16 || (K & 15) || Ns < 8 || (Ns & 7) || S < 1) return MOE_LORA_ERR_INVALID;
-  if (Ns * K > kInt32Max || S * Ns > kInt32Max) return MOE_LORA_ERR_UNSUPPORTED;
+  if (K > kMaxK || Ns * K > kInt32Max || S * Ns > kInt32Max) return MOE_LORA_ERR_UNSUPPORTED;
   p->K = int32_t(K);
   p->Ns = int32_t(Ns);
   p->S = int32_t(S);

@@ -149,6 +149,226 @@ __global__ void __launch_bounds__(KW * kWave) fp8_gemm_rows_kernel(GemmParams p,
   }
 }
 
+// ---------------------------------------------------------------- many rows
+// One LDS-direct load of 16 (or 4) bytes a lane: lane i's bytes land at lds +
+// 16 i (4 i).  Inline assembly for the reason given at dma16; soff is added to
+// every lane's offset.
+__device__ __forceinline__ void tile_dma16(i32x4_t r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  int saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+      : "memory");
+}
+__device__ __forceinline__ void tile_dma4(i32x4_t r, uint32_t lds, uint32_t voff, uint32_t soff) {
+  int saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %2, %3, %4 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+      : "memory");
+}
+
+// Work item -> (block of rows, column tile).  Consecutive workgroups go to the
+// XCDs in turn, so each XCD takes one contiguous run of items and its L2 holds
+// that run's operands; within the run, kGroup blocks of rows share each column
+// tile before the next one.
+constexpr int kGroup = 4;
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t blocks, uint32_t tiles, uint32_t* blk,
+                                        uint32_t* tile) {
+  const uint32_t total = blocks * tiles, per = total / kXcds, rem = total % kXcds;
+  const uint32_t xcd = id % kXcds, i = id / kXcds;
+  const uint32_t t = xcd * per + min(xcd, rem) + i;
+  const uint32_t grp = t / (kGroup * tiles), first = grp * kGroup;
+  const uint32_t size = min(uint32_t(kGroup), blocks - first), in = t - first * tiles;
+  *blk = first + in % size;
+  *tile = in / size;
+}
+
+// WM x WN wavefronts, each 16 FM rows x 16 FN columns.  A ring of NS stages of
+// 128 of K in LDS, filled by LDS-direct loads; a stage holds the rows' bytes,
+// the columns' bytes and the rows' scales.  A row's eight 16-byte chunks are
+// permuted by an exclusive or with bits of the row number, so that the lanes
+// that read one chunk of 16 rows spread over the banks; the load applies it to
+// the source address.
+template <int WM, int WN, int FM, int FN, int NS, bool GROUPED>
+__global__ void __launch_bounds__(WM * WN * kWave, (WM * WN + 3) / 4)
+    fp8_gemm_tile_kernel(GemmParams p, int ntiles) {
+  constexpr int BM = WM * FM * 16, BN = WN * FN * 16, NW = WM * WN;
+  constexpr int XI = BM / 8 / NW, WI = BN / 8 / NW;  // 1 KiB loads a wavefront and stage
+  constexpr int kLoads = XI + WI + 1;
+  constexpr int kX = 0, kW = BM * 128, kS = kW + BN * 128, kStage = kS + BM * 4;
+  static_assert(XI * 8 * NW == BM && WI * 8 * NW == BN && BM % kWave == 0 && BM / kWave <= NW, "tile");
+  constexpr int kFnBits = FN == 1 ? 2 : FN == 2 ? 3 : FN == 4 ? 4 : 5;
+  __shared__ __align__(1024) uint8_t lds[NS * kStage];
+
+  const uint32_t tiles = uint32_t(p.S) * ntiles;
+  uint32_t blk, tile, blocks = uint32_t(p.blocks);
+  if constexpr (GROUPED) blocks = min(blocks, uint32_t(p.ntpp[0]) / BM);
+  if (blockIdx.x >= blocks * tiles) return;
+  tile_of(blockIdx.x, blocks, tiles, &blk, &tile);
+  int64_t e = 0;
+  if constexpr (GROUPED) {
+    e = p.eids[blk];
+    if (e < 0 || e >= p.E) return;
+  }
+  const int slice = tile / ntiles, n0 = (tile % ntiles) * BN;
+  const int64_t first = int64_t(blk) * BM;
+  const int lane = lane_id(), w = wave_id(), wm = w / WN, wn = w % WN;
+  const int a = lane & 15, g = lane >> 4;
+
+  const int64_t mat = e * p.S + slice;
+  const i32x4_t wr = dma_rsrc(p.w + mat * p.Ns * int64_t(p.K), uint32_t(p.Ns) * uint32_t(p.K));
+  const int64_t x0 = GROUPED ? 0 : first;
+  const int64_t xrows = GROUPED ? p.rows : std::min<int64_t>(p.rows - first, BM);
+  const i32x4_t xr = dma_rsrc(p.x + x0 * p.K, uint32_t(xrows * p.K));
+  const i32x4_t sr = dma_rsrc(p.xs + x0, uint32_t(((p.KB - 1) * p.rows + xrows) * 4));
+  uint32_t xoff[XI], woff[WI], soff;
+  const int rl = lane >> 3, cl = lane & 7;  // row within a load, chunk as stored
+#pragma unroll
+  for (int i = 0; i < XI; ++i) {
+    const int r = 8 * (w * XI + i) + rl;
+    const RowMap m = row_of<GROUPED>(p, first, r);
+    xoff[i] = m.x_row < 0 ? kOob : uint32_t((m.x_row - x0) * p.K) + 16 * (cl ^ (r & 7));
+  }
+#pragma unroll
+  for (int i = 0; i < WI; ++i) {
+    const int r = 8 * (w * WI + i) + rl, n = n0 + r;
+    const int sw = (r & 3) | (((r >> kFnBits) & 1) << 2);
+    woff[i] = n >= p.Ns ? kOob : uint32_t(n) * uint32_t(p.K) + 16 * (cl ^ sw);
+  }
+  const int seg = w % (BM / kWave);
+  {
+    const RowMap m = row_of<GROUPED>(p, first, seg * kWave + lane);
+    soff = m.x_row < 0 ? kOob : uint32_t((m.x_row - x0) * 4);
+  }
+  const uint32_t base = lds_address(lds);
+  const int tail = p.K & (kScaleBlock - 1);  // bytes of K in a short last block
+  const uint32_t kstride = uint32_t(p.rows) * 4;
+
+  auto load = [&](int kb) {
+    const uint32_t st = base + uint32_t(kb % NS) * kStage;
+    const uint32_t k = uint32_t(kb) * kScaleBlock;
+    if (kb < p.KB - 1 || (kb == p.KB - 1 && tail == 0)) {
+#pragma unroll
+      for (int i = 0; i < XI; ++i) tile_dma16(xr, st + kX + 1024 * (w * XI + i), xoff[i], k);
+#pragma unroll
+      for (int i = 0; i < WI; ++i) tile_dma16(wr, st + kW + 1024 * (w * WI + i), woff[i], k);
+      tile_dma4(sr, st + kS + 256 * seg, soff, uint32_t(kb) * kstride);
+    } else {
+      // the short last block (chunks past K are zeros), or a stage past the
+      // end, loaded from nowhere so that every stage counts the same loads
+      const int have = kb == p.KB - 1 ? tail : 0;
+      const uint32_t kk = have ? k : 0;
+#pragma unroll
+      for (int i = 0; i < XI; ++i) {
+        const int r = 8 * (w * XI + i) + rl;
+        tile_dma16(xr, st + kX + 1024 * (w * XI + i), 16 * (cl ^ (r & 7)) < have ? xoff[i] : kOob, kk);
+      }
+#pragma unroll
+      for (int i = 0; i < WI; ++i) {
+        const int r = 8 * (w * WI + i) + rl;
+        const int sw = (r & 3) | (((r >> kFnBits) & 1) << 2);
+        tile_dma16(wr, st + kW + 1024 * (w * WI + i), 16 * (cl ^ sw) < have ? woff[i] : kOob, kk);
+      }
+      tile_dma4(sr, st + kS + 256 * seg, have ? soff : kOob, have ? uint32_t(kb) * kstride : 0);
+    }
+  };
+
+  // this wavefront's columns lie in one scale block: lane i keeps that of
+  // K block i of the current 64
+  const int nblk = std::min((n0 + wn * FN * 16) / kScaleBlock, p.NB - 1);
+  const float* wscale = p.ws + (mat * p.NB + nblk) * p.KB;
+  float wsv = lane < p.KB ? wscale[lane] : 0.0f;
+
+  f32x4_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int f = 0; f < FN; ++f) acc[i][f] = f32x4_t{0, 0, 0, 0};
+
+  const int xrow = wm * FM * 16 + a, wrow = wn * FN * 16 + 4 * FN * (a >> 2) + (a & 3);
+  const int xo = kX + xrow * 128 + 16 * (g ^ (a & 7));
+  const int wo = kW + wrow * 128 + 16 * (g ^ (a & 7));
+
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) load(s);
+  for (int kb = 0; kb < p.KB; ++kb) {
+    if ((kb & 63) == 0 && kb > 0) wsv = kb + lane < p.KB ? wscale[kb + lane] : 0.0f;
+    stage_barrier<(NS - 2) * kLoads>();
+    load(kb + NS - 1);
+    const uint8_t* st = lds + (kb % NS) * kStage;
+    const float sw = __uint_as_float(
+        __builtin_amdgcn_readlane(__float_as_uint(wsv), kb & 63));
+    i32x8_t wf[FN];
+#pragma unroll
+    for (int f = 0; f < FN; ++f)
+      wf[f] = join(*reinterpret_cast<const uint4*>(st + wo + 512 * f),
+                   *reinterpret_cast<const uint4*>(st + (wo ^ 64) + 512 * f));
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const i32x8_t xf = join(*reinterpret_cast<const uint4*>(st + xo + 2048 * i),
+                              *reinterpret_cast<const uint4*>(st + (xo ^ 64) + 2048 * i));
+      const float sx = *reinterpret_cast<const float*>(st + kS + 4 * (xrow + 16 * i)) * sw;
+      f32x4_t d[FN];
+#pragma unroll
+      for (int f = 0; f < FN; ++f) d[f] = mfma_e4m3(wf[f], xf);
+#pragma unroll
+      for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][f][j] = fmaf(d[f][j], sx, acc[i][f][j]);
+    }
+  }
+
+  // no load into LDS outlives its workgroup
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  const int nl = n0 + wn * FN * 16 + 4 * FN * g;  // this lane's 4 FN columns
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const RowMap m = row_of<GROUPED>(p, first, xrow + 16 * i);
+    if (m.y_row < 0) continue;
+    float wt = 1.0f;
+    if constexpr (GROUPED) {
+      if (p.wt) wt = p.wt[m.y_row];
+    }
+    uint16_t* out = p.y + m.y_row * (int64_t(p.S) * p.Ns) + int64_t(slice) * p.Ns + nl;
+    if constexpr (FN == 1) {
+      const f32x4_t v = acc[i][0] * wt;
+      if (nl < p.Ns)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int f = 0; f < FN; f += 2) {
+        const f32x4_t u = acc[i][f] * wt, v = acc[i][f + 1] * wt;
+        if (nl + 4 * f < p.Ns)
+          *reinterpret_cast<uint4*>(out + 4 * f) =
+              make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]),
+                         pack_bf16x2(v[2], v[3]));
+      }
+    }
+  }
+}
+
+template <int WM, int WN, int FM, int FN, int NS, bool GROUPED>
+hipError_t tile_launch(GemmParams p, hipStream_t st) {
+  constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
+  if (!GROUPED) p.blocks = int32_t((p.M + BM - 1) / BM);
+  const int ntiles = (p.Ns + BN - 1) / BN;
+  const int64_t grid = int64_t(p.blocks) * p.S * ntiles;
+  hipLaunchKernelGGL((fp8_gemm_tile_kernel<WM, WN, FM, FN, NS, GROUPED>), dim3(unsigned(grid)),
+                     dim3(WM * WN * kWave), 0, st, p, ntiles);
+  return hipGetLastError();
+}
+
 template <int MT, int NT, int KW, bool GROUPED>
 hipError_t rows_of(const GemmParams& p, hipStream_t st) {
   const int ntiles = (p.Ns + 16 * NT - 1) / (16 * NT);
@@ -161,6 +381,7 @@ hipError_t rows_of(const GemmParams& p, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
+  if (p.M > 64) return tile_launch<2, 4, 8, 4, 2, false>(p, st);
   const int rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
   p.blocks = int32_t((p.M + rows - 1) / rows);
   if (rows == 16) return rows_of<1, 1, 8, false>(p, st);
@@ -171,8 +392,8 @@ hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
 hipError_t launch_fp8_moe_gemm(GemmParams p, hipStream_t st) {
   if (p.block_m == 16) return rows_of<1, 1, 8, true>(p, st);
   if (p.block_m == 32) return rows_of<2, 1, 8, true>(p, st);
-  if (p.block_m == 64) return rows_of<4, 1, 8, true>(p, st);
-  return rows_of<8, 1, 4, true>(p, st);
+  if (p.block_m == 64) return tile_launch<1, 4, 4, 4, 2, true>(p, st);
+  return tile_launch<1, 4, 8, 4, 2, true>(p, st);
 }
 
 }  // namespace mlr
