@@ -447,34 +447,28 @@ def alloc_fp8_rows(M: int, K: int, device) -> Fp8Rows:
                    torch.empty((fp8_blocks(K), M), dtype=torch.float32, device=device))
 
 
-def _check_shape(t, name, dtype, device, shape):
-    """_check with the shape; the message is formed only for a call that is refused."""
-    if (t.__class__.__name__ in ("Tensor", "Parameter") and t.dtype is dtype
-            and tuple(t.shape) == shape and t.is_contiguous() and t.device == device):
-        return
+def _refuse(t, name, dtype, device, shape):
+    """Raise for a tensor that is not contiguous, of this type and shape, on this device."""
     _check(t, name, dtype, device)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _launch(name, device, stream, *args):
+def _launch(fn, name, device, stream, *args):
     """Call an entry point on `device`: its stream last, that device current."""
     import torch
-    if device.type != "cuda":
+    index = device.index
+    if index is None or device.type != "cuda":
         raise ValueError(f"{name} needs tensors on a GPU, got {device}")
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, expected {device}")
-    if torch.cuda.current_device() != device.index:
+    # the raw handles: a Stream object costs more than the rest of the call
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(device):
-            return _launch(name, device, stream, *args)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    rc = getattr(lib(), name)(*args, s.cuda_stream)
+            return _launch(fn, name, device, stream, *args)
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if rc != OK:
         raise MoeLoraError(rc, name)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def moe_lora_rms_norm_fp8(x, weight, *, eps: float = 1e-6, residual=None, residual_out=None, y=None,
@@ -486,23 +480,38 @@ def moe_lora_rms_norm_fp8(x, weight, *, eps: float = 1e-6, residual=None, residu
     _check(x, "x", bf, dev)
     if x.dim() != 2:
         raise ValueError("x must be [M, H]")
-    M, H = x.shape
-    _check_shape(weight, "weight", bf, dev, (H,))
-    if residual is not None:
-        _check_shape(residual, "residual", bf, dev, (M, H))
-        residual_out = residual if residual_out is None else residual_out
-        _check_shape(residual_out, "residual_out", bf, dev, (M, H))
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    if y is not None:
-        _check_shape(y, "y", bf, dev, (M, H))
+    shape = M, H = x.shape
     if out is None:
         out = alloc_fp8_rows(M, H, dev)
-    _check_shape(out.q, "out.q", torch.float8_e4m3fn, dev, (M, H))
-    _check_shape(out.scales, "out.scales", torch.float32, dev, (fp8_blocks(H), M))
-    _launch("moe_lora_rms_norm_fp8", dev, stream, _ptr(x), _ptr(residual), _ptr(weight), M, H, eps,
-            _ptr(residual_out), _ptr(y), _ptr(out.q), _ptr(out.scales))
+    q, scales = out.q, out.scales
+    ptr = [x.data_ptr(), None, None, None]
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    elif residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    for i, t, name in ((1, residual, "residual"), (2, residual_out, "residual_out"), (3, y, "y")):
+        if t is not None:
+            if t.dtype is not bf or t.shape != shape or not t.is_contiguous() or t.device != dev:
+                _refuse(t, name, bf, dev, shape)
+            ptr[i] = t.data_ptr()
+    if (weight.dtype is not bf or weight.shape != (H,) or not weight.is_contiguous()
+            or weight.device != dev):
+        _refuse(weight, "weight", bf, dev, (H,))
+    _check_rows(q, scales, "out", M, H, dev)
+    _launch(lib().moe_lora_rms_norm_fp8, "moe_lora_rms_norm_fp8", dev, stream, ptr[0], ptr[1],
+            weight.data_ptr(), M, H, eps, ptr[2], ptr[3], q.data_ptr(), scales.data_ptr())
     return out
+
+
+def _check_rows(q, scales, name, M, K, dev):
+    import torch
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    if q.dtype is not f8 or q.shape != (M, K) or not q.is_contiguous() or q.device != dev:
+        _refuse(q, name + ".q", f8, dev, (M, K))
+    kb = -(-K // FP8_BLOCK)
+    if (scales.dtype is not f32 or scales.shape != (kb, M) or not scales.is_contiguous()
+            or scales.device != dev):
+        _refuse(scales, name + ".scales", f32, dev, (kb, M))
 
 
 def moe_lora_silu_mul_fp8(y, *, h=None, out: Fp8Rows | None = None, stream=None) -> Fp8Rows:
@@ -515,35 +524,46 @@ def moe_lora_silu_mul_fp8(y, *, h=None, out: Fp8Rows | None = None, stream=None)
         raise ValueError("y must be [..., 2 * I]")
     I = y.shape[-1] // 2
     P = y.numel() // max(1, 2 * I)
-    if h is not None:
-        _check_shape(h, "h", torch.bfloat16, dev, (P, I))
+    if h is not None and (h.dtype is not torch.bfloat16 or h.shape != (P, I)
+                          or not h.is_contiguous() or h.device != dev):
+        _refuse(h, "h", torch.bfloat16, dev, (P, I))
     if out is None:
         out = alloc_fp8_rows(P, I, dev)
-    _check_shape(out.q, "out.q", torch.float8_e4m3fn, dev, (P, I))
-    _check_shape(out.scales, "out.scales", torch.float32, dev, (fp8_blocks(I), P))
-    _launch("moe_lora_silu_mul_fp8", dev, stream, _ptr(y), P, I, _ptr(h), _ptr(out.q),
-            _ptr(out.scales))
+    q, scales = out.q, out.scales
+    _check_rows(q, scales, "out", P, I, dev)
+    _launch(lib().moe_lora_silu_mul_fp8, "moe_lora_silu_mul_fp8", dev, stream, y.data_ptr(), P, I,
+            None if h is None else h.data_ptr(), q.data_ptr(), scales.data_ptr())
     return out
+
+
+def _check_weights(w, w_scales, dev):
+    import torch
+    _check(w, "w", torch.float8_e4m3fn, dev)
+    *lead, Ns, K = w.shape
+    shape = (*lead, -(-Ns // FP8_BLOCK), -(-K // FP8_BLOCK))
+    if (w_scales.dtype is not torch.float32 or w_scales.shape != shape
+            or not w_scales.is_contiguous() or w_scales.device != dev):
+        _refuse(w_scales, "w_scales", torch.float32, dev, shape)
 
 
 def moe_lora_fp8_gemm(x: Fp8Rows, w, w_scales, y=None, *, stream=None):
     """8-bit rows times w [S, Ns, K] (e4m3, a scale per 128 x 128 block of a slice); y bf16
     [M, S*Ns] is allocated when not given; see moe_lora.h."""
     import torch
-    f8, dev = torch.float8_e4m3fn, w.device
-    _check(w, "w", f8, dev)
-    if w.dim() != 3 or x.q.dim() != 2:
+    dev, xq, xs = w.device, x.q, x.scales
+    if w.dim() != 3 or xq.dim() != 2:
         raise ValueError("w must be [S, Ns, K] and x.q [M, K]")
     S, Ns, K = w.shape
-    M = x.q.shape[0]
-    _check_shape(w_scales, "w_scales", torch.float32, dev, (S, fp8_blocks(Ns), fp8_blocks(K)))
-    _check_shape(x.q, "x.q", f8, dev, (M, K))
-    _check_shape(x.scales, "x.scales", torch.float32, dev, (fp8_blocks(K), M))
+    M = xq.shape[0]
+    _check_weights(w, w_scales, dev)
+    _check_rows(xq, xs, "x", M, K, dev)
     if y is None:
         y = torch.empty((M, S * Ns), dtype=torch.bfloat16, device=dev)
-    _check_shape(y, "y", torch.bfloat16, dev, (M, S * Ns))
-    _launch("moe_lora_fp8_gemm", dev, stream, _ptr(x.q), _ptr(x.scales), _ptr(w), _ptr(w_scales),
-            M, K, Ns, S, _ptr(y))
+    elif (y.dtype is not torch.bfloat16 or y.shape != (M, S * Ns) or not y.is_contiguous()
+          or y.device != dev):
+        _refuse(y, "y", torch.bfloat16, dev, (M, S * Ns))
+    _launch(lib().moe_lora_fp8_gemm, "moe_lora_fp8_gemm", dev, stream, xq.data_ptr(), xs.data_ptr(),
+            w.data_ptr(), w_scales.data_ptr(), M, K, Ns, S, y.data_ptr())
     return y
 
 
@@ -552,27 +572,32 @@ def moe_lora_fp8_moe_gemm(x: Fp8Rows, w, w_scales, align: AlignOutput, topk_weig
     """8-bit rows times each routed pair's expert of w [E, S, Ns, K], into y [M, topk, S*Ns]; align
     is one slot's (L = 1); see moe_lora.h."""
     import torch
-    f8, i32, dev = torch.float8_e4m3fn, torch.int32, y.device
+    i32, dev, xq, xs = torch.int32, y.device, x.q, x.scales
     _check(y, "y", torch.bfloat16, dev)
-    _check(w, "w", f8, dev)
-    if w.dim() != 4 or y.dim() != 3 or x.q.dim() != 2:
+    if w.dim() != 4 or y.dim() != 3 or xq.dim() != 2:
         raise ValueError("w must be [E, S, Ns, K], y [M, topk, S*Ns] and x.q [rows, K]")
     E, S, Ns, K = w.shape
     M, topk, N = y.shape
     if N != S * Ns:
         raise ValueError("y's last dim must be S*Ns")
-    rows, kb = M * topk if x_per_pair else M, fp8_blocks(K)
-    _check_shape(w_scales, "w_scales", torch.float32, dev, (E, S, fp8_blocks(Ns), kb))
-    _check_shape(x.q, "x.q", f8, dev, (rows, K))
-    _check_shape(x.scales, "x.scales", torch.float32, dev, (kb, rows))
+    _check_weights(w, w_scales, dev)
+    _check_rows(xq, xs, "x", M * topk if x_per_pair else M, K, dev)
+    tw = None
     if topk_weights is not None:
-        _check_shape(topk_weights, "topk_weights", torch.float32, dev, (M, topk))
-    cap = align_capacity(M, topk, E, align.block_m)
-    _check_shape(align.sorted_token_ids, "align.sorted_token_ids", i32, dev, (1, cap))
-    _check_shape(align.expert_ids, "align.expert_ids", i32, dev, (1, cap // align.block_m))
-    _check_shape(align.num_tokens_post_padded, "align.num_tokens_post_padded", i32, dev, (1,))
-    _launch("moe_lora_fp8_moe_gemm", dev, stream, _ptr(x.q), _ptr(x.scales),
-            int(bool(x_per_pair)), _ptr(w), _ptr(w_scales), _ptr(align.sorted_token_ids),
-            _ptr(align.expert_ids), _ptr(align.num_tokens_post_padded), _ptr(topk_weights),
-            int(bool(mul_routed_weight)), M, topk, K, Ns, S, E, align.block_m, _ptr(y))
+        if (topk_weights.dtype is not torch.float32 or topk_weights.shape != (M, topk)
+                or not topk_weights.is_contiguous() or topk_weights.device != dev):
+            _refuse(topk_weights, "topk_weights", torch.float32, dev, (M, topk))
+        tw = topk_weights.data_ptr()
+    block_m = align.block_m
+    cap = align_capacity(M, topk, E, block_m)
+    ids, eids, ntpp = align.sorted_token_ids, align.expert_ids, align.num_tokens_post_padded
+    for t, name, shape in ((ids, "sorted_token_ids", (1, cap)),
+                           (eids, "expert_ids", (1, cap // block_m)),
+                           (ntpp, "num_tokens_post_padded", (1,))):
+        if t.dtype is not i32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            _refuse(t, "align." + name, i32, dev, shape)
+    _launch(lib().moe_lora_fp8_moe_gemm, "moe_lora_fp8_moe_gemm", dev, stream, xq.data_ptr(),
+            xs.data_ptr(), 1 if x_per_pair else 0, w.data_ptr(), w_scales.data_ptr(),
+            ids.data_ptr(), eids.data_ptr(), ntpp.data_ptr(), tw, 1 if mul_routed_weight else 0,
+            M, topk, K, Ns, S, E, block_m, y.data_ptr())
     return y
