@@ -57,7 +57,8 @@ struct GemmParams {
   const int32_t* ntpp;    // [1]
   const float* wt;        // [M topk]; null: not applied
   int32_t numel, topk, E, block_m, x_per_pair;
-  int32_t blocks;         // blocks of rows the grid covers
+  int32_t blocks;         // align blocks: at most this many, of this launch
+  int32_t block0;         // and its first
 };
 
 hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st);      // dense

@@ -47,7 +47,7 @@ struct RowMap {
 template <bool GROUPED>
 __device__ __forceinline__ RowMap row_of(const GemmParams& p, int64_t first, int i) {
   if constexpr (GROUPED) {
-    const uint32_t pair = i < p.block_m ? uint32_t(p.sorted[first + i]) : uint32_t(p.numel);
+    const uint32_t pair = uint32_t(p.sorted[first + i]);
     if (pair >= uint32_t(p.numel)) return {-1, -1};
     return {int64_t(p.x_per_pair ? pair : pair / uint32_t(p.topk)), int64_t(pair)};
   } else {
@@ -64,15 +64,15 @@ template <int MT, int NT, int KW, int U, bool GROUPED>
 __global__ void __launch_bounds__(KW * kWave) fp8_gemm_rows_kernel(GemmParams p, int ntiles) {
   __shared__ f32x4_t red[KW][MT * NT][kWave];
   const int tile = blockIdx.x % (p.S * ntiles);
-  const int blk = blockIdx.x / (p.S * ntiles);
+  const int64_t first = int64_t(blockIdx.x / (p.S * ntiles)) * 16 * MT;
   int64_t e = 0;
   if constexpr (GROUPED) {
-    if (int64_t(blk) * p.block_m >= p.ntpp[0]) return;
-    e = p.eids[blk];
+    // a block's pairs come first, its padding last: pieces of padding end here
+    if (first >= p.ntpp[0] || uint32_t(p.sorted[first]) >= uint32_t(p.numel)) return;
+    e = p.eids[first / p.block_m];
     if (e < 0 || e >= p.E) return;
   }
   const int slice = tile / ntiles, n0 = (tile % ntiles) * 16 * NT;
-  const int64_t first = GROUPED ? int64_t(blk) * p.block_m : int64_t(blk) * 16 * MT;
   const int lane = lane_id(), w = wave_id(), a = lane & 15, g = lane >> 4;
 
   const uint8_t* wbase = p.w + (e * p.S + slice) * p.Ns * int64_t(p.K);
@@ -185,28 +185,120 @@ __device__ __forceinline__ void tile_dma4(i32x4_t r, uint32_t lds, uint32_t voff
       : "memory");
 }
 
-// Work item -> (block of rows, column tile).  Workgroups go to the XCDs in
+// stage_barrier<VM>, or, where `young` is not 0, one that also leaves the ST
+// stores of the last tile in flight.  They are younger than the loads waited
+// for, and memory operations complete in order, so waiting for VM would wait
+// for them too.  One asm statement, to keep the loop around it one block.
+template <int VM, int ST>
+__device__ __forceinline__ void ring_barrier(int young) {
+  static_assert(VM + ST < 64, "vmcnt is a 6-bit field");
+  asm volatile(
+      "s_cmp_eq_u32 %0, 0\n\t"
+      "s_cbranch_scc1 0f\n\t"
+      "s_waitcnt vmcnt(%2) lgkmcnt(0)\n\t"
+      "s_branch 1f\n"
+      "0:\n\t"
+      "s_waitcnt vmcnt(%1) lgkmcnt(0)\n"
+      "1:\n\t"
+      "s_barrier"
+      :
+      : "s"(young), "n"(VM), "n"(VM + ST)
+      : "memory", "scc");
+}
+
+// Work item -> (tile of rows, tile of columns).  Workgroups go to the XCDs in
 // turn, so each XCD takes one contiguous run of items, its workgroups in turn;
-// its L2 then holds that run's operands.  Within the run kGroup blocks of rows
+// its L2 then holds that run's operands.  Within the run kGroup tiles of rows
 // share each column tile before the next one.
 constexpr int kGroup = 4;
 struct Items {
-  uint32_t blocks, tiles;  // blocks of rows, column tiles (of all slices)
-  uint32_t first, end;     // this XCD's run
-  uint32_t step;           // its workgroups
+  uint32_t rows, cols;  // tiles of rows, tiles of columns (of all slices)
+  uint32_t first, end;  // this XCD's run
+  uint32_t step;        // its workgroups
 
-  __device__ __forceinline__ Items(uint32_t b, uint32_t t) : blocks(b), tiles(t) {
-    const uint32_t total = b * t, per = total / kXcds, rem = total % kXcds;
+  __device__ __forceinline__ Items(uint32_t r, uint32_t c) : rows(r), cols(c) {
+    const uint32_t total = r * c, per = total / kXcds, rem = total % kXcds;
     const uint32_t xcd = blockIdx.x % kXcds;
     first = xcd * per + min(xcd, rem);
     end = first + per + (xcd < rem ? 1 : 0);
     step = (gridDim.x - xcd + kXcds - 1) / kXcds;
   }
-  __device__ __forceinline__ void at(uint32_t t, uint32_t* blk, uint32_t* tile) const {
-    const uint32_t grp = t / (kGroup * tiles), base = grp * kGroup;
-    const uint32_t size = min(uint32_t(kGroup), blocks - base), in = t - base * tiles;
-    *blk = base + in % size;
-    *tile = in / size;
+  __device__ __forceinline__ void at(uint32_t t, uint32_t* row, uint32_t* col) const {
+    const uint32_t grp = t / (kGroup * cols), base = grp * kGroup;
+    const uint32_t size = min(uint32_t(kGroup), rows - base), in = t - base * cols;
+    *row = base + in % size;
+    *col = in / size;
+  }
+};
+
+// Grouped: a tile of BM rows takes up to BM / block_m consecutive blocks of one
+// expert, so that its weights are read once for all of them.  The first block
+// of each tile is found on chip: in every run of blocks with the same expert,
+// each (BM / block_m)-th.  Each 64 blocks keep their first blocks as a mask and
+// the count of those before them; a launch takes at most kTileBlocks blocks.
+constexpr int kTileChunks = 256;
+constexpr int kTileBlocks = kTileChunks * kWave;
+struct TileList {
+  uint64_t lead[kTileChunks];
+  uint32_t before[kTileChunks];
+
+  // The whole workgroup; `starts` is LDS scratch of kTileChunks masks.
+  // Returns the number of tiles.
+  __device__ inline uint32_t build(const int32_t* eids, int blocks, int E, int per, uint64_t* starts,
+                                   int nw) {
+    const int lane = lane_id(), w = wave_id(), chunks = (blocks + kWave - 1) / kWave;
+    for (int c = w; c < chunks; c += nw) {
+      const int i = c * kWave + lane;
+      const bool in = i < blocks;
+      const uint64_t m = __ballot(in && (i == 0 || eids[i] != eids[i - 1]));
+      if (lane == 0) starts[c] = m;
+    }
+    __syncthreads();
+    for (int c = w; c < kTileChunks; c += nw) {
+      uint64_t m = 0;
+      if (c < chunks) {
+        int run = 0;  // where the run that reaches into this chunk began
+        for (int b = c - 1; b >= 0; --b) {
+          if (starts[b]) {
+            run = b * kWave + 63 - __builtin_clzll(starts[b]);
+            break;
+          }
+        }
+        const int i = c * kWave + lane;
+        const uint64_t own = starts[c] & (lanes_below(lane) | (uint64_t(1) << lane));
+        if (own) run = c * kWave + 63 - __builtin_clzll(own);
+        m = __ballot(i < blocks && uint32_t(eids[i < blocks ? i : 0]) < uint32_t(E) &&
+                     (i - run) % per == 0);
+      }
+      if (lane == 0) lead[c] = m;
+    }
+    __syncthreads();
+    constexpr int kEach = kTileChunks / kWave;
+    uint32_t n[kEach], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      n[j] = sum;
+      sum += __builtin_popcountll(lead[lane * kEach + j]);
+    }
+    const uint32_t incl = uint32_t(wave_incl_scan(int(sum)));
+    if (w == 0) {
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) before[lane * kEach + j] = incl - sum + n[j];
+    }
+    const uint32_t total = uint32_t(lane_value(int(incl), kWave - 1));
+    __syncthreads();
+    return total;
+  }
+  // Block of tile t.
+  __device__ __forceinline__ int block(uint32_t t) const {
+    constexpr int kEach = kTileChunks / kWave;
+    const int lane = lane_id();
+    const int hi = __builtin_popcountll(__ballot(before[lane * kEach] <= t)) - 1;
+    const int lo = __builtin_popcountll(__ballot(lane < kEach && before[hi * kEach + lane % kEach] <= t)) - 1;
+    const int c = hi * kEach + lo;
+    const uint64_t m = lead[c];
+    const bool here = (m >> lane & 1) && __builtin_popcountll(m & lanes_below(lane)) == int(t - before[c]);
+    return c * kWave + __builtin_ctzll(__ballot(here));
   }
 };
 
@@ -226,16 +318,18 @@ struct Tile {
   static constexpr int XI = BM / 8 / NW, WI = BN / 8 / NW;  // 1 KiB loads a wavefront and stage
   static constexpr int kLoads = XI + WI + 1;
   static constexpr int kX = 0, kW = BM * 128, kS = kW + BN * 128, kStage = kS + BM * 4 + 256;
-  // tiles the loads run ahead by, and this one: the pairs of their rows
-  static constexpr int kPairs = NS * kStage, kRing = NS + 1;
-  static constexpr int lds_bytes(bool grouped) { return kPairs + (grouped ? kRing * BM * 4 : 0); }
+  // tiles the loads run ahead by, and this one: their rows' pairs and weights
+  static constexpr int kPairs = NS * kStage, kRing = NS + 1, kList = kPairs + kRing * BM * 8;
+  static constexpr int lds_bytes(bool grouped) {
+    return grouped ? kList + int(sizeof(TileList)) : kPairs;
+  }
   // workgroups of a CU, by LDS and by two wavefronts a SIMD
   static constexpr int groups(bool grouped) {
     const int a = 160 * 1024 / lds_bytes(grouped), b = 8 / NW;
     return a < b ? a : b;
   }
   static_assert(XI * 8 * NW == BM && WI * 8 * NW == BN && BM % kWave == 0, "tile");
-  static_assert(BM / kWave < NW && FM % 2 == 0 && NS >= 2, "tile");
+  static_assert(BM / kWave < NW && FM % 2 == 0 && FN % 2 == 0 && NS >= 2, "tile");
 };
 
 template <int WM, int WN, int FM, int FN, int NS, bool GROUPED>
@@ -244,90 +338,101 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   using T = Tile<WM, WN, FM, FN, NS>;
   constexpr int BM = T::BM, BN = T::BN, XI = T::XI, WI = T::WI, kLoads = T::kLoads;
   constexpr int kX = T::kX, kW = T::kW, kS = T::kS, kStage = T::kStage;
-  constexpr int kFnBits = FN == 1 ? 2 : FN == 2 ? 3 : FN == 4 ? 4 : 5;
   __shared__ __align__(1024) uint8_t lds[T::lds_bytes(GROUPED)];
 
-  uint32_t blocks = uint32_t(p.blocks);
-  if constexpr (GROUPED) blocks = min(blocks, uint32_t(p.ntpp[0]) / BM);
-  const Items items(blocks, uint32_t(p.S) * ntiles);
+  TileList* list = reinterpret_cast<TileList*>(lds + T::kList);
+  int blocks = 0;  // grouped: blocks of this launch
+  uint32_t row_tiles;
+  if constexpr (GROUPED) {
+    blocks = std::min(p.blocks, p.ntpp[0] / p.block_m - p.block0);
+    if (blocks <= 0) return;
+    row_tiles = list->build(p.eids + p.block0, blocks, p.E, BM / p.block_m,
+                            reinterpret_cast<uint64_t*>(lds), T::NW);
+  } else {
+    row_tiles = uint32_t((p.M + BM - 1) / BM);
+  }
+  const Items items(row_tiles, uint32_t(p.S) * ntiles);
   const int lane = lane_id(), w = wave_id(), wm = w / WN, wn = w % WN;
   const int a = lane & 15, g = lane >> 4;
   const int rl = lane >> 3, cl = lane & 7;  // row within a load, chunk as stored
-  auto swizzle = [](int r) { return (r & 3) | (((r >> kFnBits) & 1) << 2); };
-  auto expert = [&](uint32_t blk) { return GROUPED ? p.eids[blk] : 0; };
-  // the item from t on whose expert is one (the run's end if there is none)
-  auto valid = [&](uint32_t t) {
-    if constexpr (GROUPED) {
-      for (; t < items.end; t += items.step) {
-        uint32_t blk, tile;
-        items.at(t, &blk, &tile);
-        if (uint32_t(p.eids[blk]) < uint32_t(p.E)) break;
-      }
-    }
-    return t;
-  };
+  auto swizzle = [](int r) { return (r & 3) | ((r >> 1) & 4); };  // bits 0, 1, 3
 
   // ---- the loading side: its tile, and how far it is
-  uint32_t lt = valid(items.first + blockIdx.x / kXcds);
+  uint32_t lt = items.first + blockIdx.x / kXcds;
   uint32_t ct = lt;  // the tile being multiplied
   if (lt >= items.end) return;
   int lkb = 0, lstage = 0, lring = 0;
   i32x4_t wr, xr, sr;
-  // Offsets of this lane's chunks: grouped rows lie anywhere; dense rows and
-  // the columns follow each other, 8 rows a load (the columns' chunk order has
-  // two forms), and what is behind the last row is behind the resource's range.
-  constexpr int kXoff = GROUPED ? XI : 1;
-  uint32_t xoff[kXoff], woff[2], soff;
+  // A load takes 8 rows, 8 chunks of each.  Dense rows and the columns follow
+  // each other, and what is behind the last one is behind the resource's range;
+  // grouped rows lie anywhere: lane i keeps the offset of this wavefront's row
+  // i.  The columns' chunk order has two forms, by bit 3 of the column.
+  const int xc = 16 * (cl ^ rl), wc = 16 * (cl ^ swizzle(rl));
+  uint32_t xoff, woff, soff;
   constexpr int kSegs = BM / kWave, kCols = (BN + kScaleBlock - 1) / kScaleBlock;
   const int sdst = kS + 256 * std::min(w, kSegs);
   const uint32_t sstride = w < kSegs ? uint32_t(p.rows) * 4 : 4;
   const uint32_t step8 = 8 * uint32_t(p.K);
   const uint32_t base = lds_address(lds);
-  int32_t* pairs = reinterpret_cast<int32_t*>(lds + T::kPairs);
+  int2* pairs = reinterpret_cast<int2*>(lds + T::kPairs);
 
   auto set_tile = [&]() {
-    if (lt >= items.end) {  // nothing left: loads from nowhere
-#pragma unroll
-      for (int i = 0; i < kXoff; ++i) xoff[i] = kOob;
-      woff[0] = woff[1] = soff = kOob;
-      return;
-    }
-    uint32_t blk, tile;
-    items.at(lt, &blk, &tile);
-    const int slice = tile / ntiles, n0 = (tile % ntiles) * BN;
-    const int64_t first = int64_t(blk) * BM;
-    const int64_t mat = int64_t(expert(blk)) * p.S + slice;
-    wr = dma_rsrc(p.w + mat * p.Ns * int64_t(p.K), uint32_t(p.Ns) * uint32_t(p.K));
-    const int64_t x0 = GROUPED ? 0 : first;
-    const int64_t xrows = GROUPED ? p.rows : std::min<int64_t>(p.rows - first, BM);
-    xr = dma_rsrc(p.x + x0 * p.K, uint32_t(xrows * p.K));
-#pragma unroll
-    for (int i = 0; i < kXoff; ++i) {
-      const int r = 8 * (w * XI + i) + rl;
+    uint32_t nx = kOob, nw = kOob, ns = kOob;  // nothing left: loads from nowhere
+    if (lt < items.end) {
+      // not to be computed once and kept: the registers are needed
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      uint32_t row, tile;
+      items.at(lt, &row, &tile);
+      const int slice = tile / ntiles, n0 = (tile % ntiles) * BN;
+      int64_t first = int64_t(row) * BM, mat = slice;
+      const int32_t* eids = p.eids + p.block0;
+      int blk = 0, e = 0;
       if constexpr (GROUPED) {
-        const RowMap m = row_of<GROUPED>(p, first, r);
-        xoff[i] = m.x_row < 0 ? kOob : uint32_t(m.x_row * p.K) + 16 * (cl ^ rl);
+        blk = list->block(row);
+        e = eids[blk];
+        first = int64_t(p.block0 + blk) * p.block_m;
+        mat += int64_t(e) * p.S;
+      }
+      // row i of the tile; a grouped tile ends where its expert does
+      auto row_at = [&](int i) {
+        if constexpr (GROUPED) {
+          const int b = blk + i / p.block_m;
+          if (b >= blocks || eids[b] != e) return RowMap{-1, -1};
+        }
+        return row_of<GROUPED>(p, first, i);
+      };
+      wr = dma_rsrc(p.w + mat * p.Ns * int64_t(p.K), uint32_t(p.Ns) * uint32_t(p.K));
+      const int64_t x0 = GROUPED ? 0 : first;
+      const int64_t xrows = GROUPED ? p.rows : std::min<int64_t>(p.rows - first, BM);
+      xr = dma_rsrc(p.x + x0 * p.K, uint32_t(xrows * p.K));
+      if constexpr (GROUPED) {
+        const RowMap m = row_at(8 * w * XI + ln % (8 * XI));
+        if (m.x_row >= 0) nx = uint32_t(m.x_row * p.K);
       } else {
-        xoff[i] = uint32_t(r) * uint32_t(p.K) + 16 * (cl ^ rl);
+        nx = uint32_t(8 * w * XI + (ln >> 3)) * uint32_t(p.K);
+      }
+      nw = uint32_t(n0 + 8 * w * WI + (ln >> 3)) * uint32_t(p.K);
+      // The stage's scales: the first wavefronts load those of 64 rows each,
+      // the others (all alike) those of the tile's column blocks.
+      const float* from = w < kSegs ? p.xs + x0 : p.ws + mat * p.NB * p.KB;
+      const int64_t count = w < kSegs ? (p.KB - 1) * p.rows + xrows : int64_t(p.NB) * p.KB;
+      sr = dma_rsrc(from, uint32_t(count * 4));
+      if (w < kSegs) {
+        const RowMap m = row_at(w * kWave + ln);
+        if (m.x_row >= 0) ns = uint32_t((m.x_row - x0) * 4);
+        if constexpr (GROUPED) {
+          const float wt = p.wt && m.y_row >= 0 ? p.wt[m.y_row] : 1.0f;
+          pairs[lring * BM + w * kWave + ln] = make_int2(int32_t(m.y_row), __float_as_int(wt));
+        }
+      } else {
+        const int nb = n0 / kScaleBlock + ln;
+        if (ln < kCols && nb < p.NB) ns = uint32_t(nb) * uint32_t(p.KB) * 4;
       }
     }
-    const int r = 8 * w * WI + rl;
-    const uint32_t n = uint32_t(n0 + r) * uint32_t(p.K);
-    woff[0] = n + 16 * (cl ^ swizzle(rl));
-    woff[1] = n + 16 * (cl ^ swizzle(rl) ^ 4);
-    // The stage's scales: the first wavefronts load those of 64 rows each, the
-    // others (all alike) those of the tile's column blocks.
-    const float* from = w < kSegs ? p.xs + x0 : p.ws + mat * p.NB * p.KB;
-    const int64_t count = w < kSegs ? (p.KB - 1) * p.rows + xrows : int64_t(p.NB) * p.KB;
-    sr = dma_rsrc(from, uint32_t(count * 4));
-    if (w < kSegs) {
-      const RowMap m = row_of<GROUPED>(p, first, w * kWave + lane);
-      soff = m.x_row < 0 ? kOob : uint32_t((m.x_row - x0) * 4);
-      if constexpr (GROUPED) pairs[lring * BM + w * kWave + lane] = int32_t(m.y_row);
-    } else {
-      const int nb = n0 / kScaleBlock + lane;
-      soff = lane < kCols && nb < p.NB ? uint32_t(nb) * uint32_t(p.KB) * 4 : kOob;
-    }
+    xoff = nx;
+    woff = nw;
+    soff = ns;
   };
   // One of a stage's loads.  Chunks past K in a short last block read as
   // zeros; behind the last tile everything does, so that every stage counts the
@@ -337,14 +442,14 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     const int have = p.K - lkb * kScaleBlock;
     const uint32_t k = uint32_t(lkb) * kScaleBlock;
     if (l < XI) {
-      const uint32_t m = 16 * (cl ^ rl) < have ? 0 : kOob;
-      const uint32_t o = GROUPED ? xoff[l % kXoff] : xoff[0] + uint32_t(l) * step8;
-      tile_dma16(xr, st + kX + 1024 * (w * XI + l), o | m, k);
+      const uint32_t o = GROUPED ? __builtin_amdgcn_ds_bpermute(4 * (8 * l + rl), xoff)
+                                 : xoff + uint32_t(l) * step8;
+      tile_dma16(xr, st + kX + 1024 * (w * XI + l), (o + xc) | (xc < have ? 0 : kOob), k);
     } else if (l < XI + WI) {
       const int i = l - XI;
-      const int flip = swizzle(8 * (w * WI + i)) >> 2;  // uniform: bit kFnBits of the row
-      const uint32_t m = 16 * (cl ^ swizzle(rl) ^ (4 * flip)) < have ? 0 : kOob;
-      tile_dma16(wr, st + kW + 1024 * (w * WI + i), ((flip ? woff[1] : woff[0]) + uint32_t(i) * step8) | m, k);
+      const int c = wc ^ (16 * swizzle(8 * (w * WI + i)));
+      tile_dma16(wr, st + kW + 1024 * (w * WI + i),
+                 (woff + uint32_t(i) * step8 + c) | (c < have ? 0 : kOob), k);
     } else {
       tile_dma4(sr, st + sdst, soff, uint32_t(lkb) * sstride);
     }
@@ -355,7 +460,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   };
   auto next_loads = [&]() {
     lkb = 0;
-    if (lt < items.end) lt = valid(lt + items.step);
+    if (lt < items.end) lt += items.step;
     lring = lring + 1 == T::kRing ? 0 : lring + 1;
     set_tile();
   };
@@ -368,7 +473,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
 #pragma unroll
       for (int f = 0; f < FN; ++f) acc[i][f] = f32x4_t{0, 0, 0, 0};
   };
-  const int xrow = wm * FM * 16 + a, wrow = wn * FN * 16 + 4 * FN * (a >> 2) + (a & 3);
+  const int xrow = wm * FM * 16 + a, wrow = wn * FN * 16 + 8 * (a >> 2) + (a & 3);
   const int xo = kX + xrow * 128 + 16 * (g ^ (a & 7));
   const int wo = kW + wrow * 128 + 16 * (g ^ (a & 7));
   const int so = kS + BM * 4 + wn * FN * 16 / kScaleBlock * 4;  // this wavefront's column block
@@ -387,8 +492,9 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     for (int j = 0; j < 4; ++j) acc[i][f][j] = fmaf(d[f][j], sd, acc[i][f][j]);
   };
   auto columns = [&](const uint8_t* st, int f) {
-    wf[f] = join(*reinterpret_cast<const uint4*>(st + wo + 512 * f),
-                 *reinterpret_cast<const uint4*>(st + (wo ^ 64) + 512 * f));
+    const int o = 4096 * (f >> 1) + 512 * (f & 1);
+    wf[f] = join(*reinterpret_cast<const uint4*>(st + wo + o),
+                 *reinterpret_cast<const uint4*>(st + (wo ^ 64) + o));
   };
   auto rows = [&](const uint8_t* st, int i) {
     xf[i & 1] = join(*reinterpret_cast<const uint4*>(st + xo + 2048 * i),
@@ -413,6 +519,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   sw = *reinterpret_cast<const float*>(lds + so);
   clear();
   int kb = 0, stage = 0, ring = 0;
+  int young = 0;  // stages still waited for whose loads are older than the last tile's stores
   while (true) {
     // stages until one side changes its tile
     const int n = std::min(p.KB - kb, p.KB - lkb);
@@ -426,7 +533,8 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
         if (i < FM - 1) {
           rows(st, i + 1);
         } else {
-          stage_barrier<(NS - 2) * kLoads>();
+          ring_barrier<(NS - 2) * kLoads, FM * FN / 2>(__builtin_amdgcn_readfirstlane(young));
+          young = std::max(young - 1, 0);
           rows(nx, 0);
           sw = *reinterpret_cast<const float*>(nx + so);
         }
@@ -454,39 +562,37 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
       add(FM - 1, f);
       d[f] = f32x4_t{0, 0, 0, 0};
     }
-    uint32_t blk, tile;
-    items.at(ct, &blk, &tile);
+    uint32_t row, tile;
+    items.at(ct, &row, &tile);
     const int slice = tile / ntiles;
-    const int nl = (tile % ntiles) * BN + wn * FN * 16 + 4 * FN * g;  // this lane's 4 FN columns
+    const int nl = (tile % ntiles) * BN + wn * FN * 16 + 8 * g;  // this lane's columns: 8 of each 32
+    int stores = 0;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       int64_t y;
       float wt = 1.0f;
       if constexpr (GROUPED) {
-        y = pairs[ring * BM + xrow + 16 * i];
-        if (y < 0) continue;
-        if (p.wt) wt = p.wt[y];
+        const int2 pr = pairs[ring * BM + xrow + 16 * i];
+        y = pr.x;
+        wt = __int_as_float(pr.y);
       } else {
-        y = int64_t(blk) * BM + xrow + 16 * i;
-        if (y >= p.M) continue;
+        y = int64_t(row) * BM + xrow + 16 * i;
+        if (y >= p.M) y = -1;
       }
       uint16_t* out = p.y + y * (int64_t(p.S) * p.Ns) + int64_t(slice) * p.Ns + nl;
-      if constexpr (FN == 1) {
-        const f32x4_t v = acc[i][0] * wt;
-        if (nl < p.Ns)
-          *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      } else {
 #pragma unroll
-        for (int f = 0; f < FN; f += 2) {
-          const f32x4_t u = acc[i][f] * wt, v = acc[i][f + 1] * wt;
-          if (nl + 4 * f < p.Ns)
-            *reinterpret_cast<uint4*>(out + 4 * f) =
-                make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]),
-                           pack_bf16x2(v[2], v[3]));
-        }
+      for (int f = 0; f < FN; f += 2) {
+        const f32x4_t u = acc[i][f] * wt, v = acc[i][f + 1] * wt;
+        const bool in = y >= 0 && nl + 16 * f < p.Ns;
+        stores += __ballot(in) != 0;
+        if (in)
+          *reinterpret_cast<uint4*>(out + 16 * f) =
+              make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]),
+                         pack_bf16x2(v[2], v[3]));
       }
     }
-    ct = valid(ct + items.step);
+    young = stores == FM * FN / 2 ? NS - 1 : 0;
+    ct += items.step;
     if (ct >= items.end) break;
     clear();
     kb = 0;
@@ -499,19 +605,26 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
 template <int WM, int WN, int FM, int FN, int NS, bool GROUPED>
 hipError_t tile_launch(GemmParams p, hipStream_t st) {
   using T = Tile<WM, WN, FM, FN, NS>;
-  if (!GROUPED) p.blocks = int32_t((p.M + T::BM - 1) / T::BM);
   const int ntiles = (p.Ns + T::BN - 1) / T::BN;
   const int64_t resident = int64_t(std::max(xcd_compute_units(), 1)) * kXcds * T::groups(GROUPED);
-  const int64_t grid = std::min(int64_t(p.blocks) * p.S * ntiles, resident);
-  hipLaunchKernelGGL((fp8_gemm_tile_kernel<WM, WN, FM, FN, NS, GROUPED>), dim3(unsigned(grid)),
-                     dim3(T::NW * kWave), 0, st, p, ntiles);
-  return hipGetLastError();
+  const int32_t all = GROUPED ? p.blocks : int32_t((p.M + T::BM - 1) / T::BM);
+  const int32_t most = GROUPED ? kTileBlocks : all;
+  for (p.block0 = 0; p.block0 < all; p.block0 += most) {
+    p.blocks = std::min(most, all - p.block0);
+    const int64_t grid = std::min(int64_t(p.blocks) * p.S * ntiles, resident);
+    hipLaunchKernelGGL((fp8_gemm_tile_kernel<WM, WN, FM, FN, NS, GROUPED>), dim3(unsigned(grid)),
+                       dim3(T::NW * kWave), 0, st, p, ntiles);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int MT, int NT, int KW, int U, bool GROUPED>
 hipError_t rows_of(const GemmParams& p, hipStream_t st) {
   const int ntiles = (p.Ns + 16 * NT - 1) / (16 * NT);
-  const int64_t grid = int64_t(p.blocks) * p.S * ntiles;
+  const int64_t pieces = GROUPED ? int64_t(p.blocks) * p.block_m / (16 * MT) : (p.M + 16 * MT - 1) / (16 * MT);
+  const int64_t grid = pieces * p.S * ntiles;
   hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, NT, KW, U, GROUPED>), dim3(unsigned(grid)),
                      dim3(KW * kWave), 0, st, p, ntiles);
   return hipGetLastError();
@@ -519,20 +632,43 @@ hipError_t rows_of(const GemmParams& p, hipStream_t st) {
 
 }  // namespace
 
+// The tile whose rounds over the device cost least.  A round's time for each
+// 128 of K, in hundredths of a microsecond (measured at K = 4096 with every
+// CU busy): 64 x 64 35, or 50 with two on a CU; 64 x 128 46; 128 x 128 65;
+// 128 x 256 98; 256 x 256 175.
 hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
-  if (p.M > 64) return tile_launch<2, 4, 8, 4, 2, false>(p, st);
-  const int rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
-  p.blocks = int32_t((p.M + rows - 1) / rows);
-  if (rows == 16) return rows_of<1, 1, 8, 2, false>(p, st);
-  if (rows == 32) return rows_of<2, 1, 8, 1, false>(p, st);
-  return rows_of<4, 1, 8, 1, false>(p, st);
+  const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
+  // Few rows: 16 columns a workgroup while that is not much over one a CU
+  // (4096 columns, K = 4096: 16 rows 6.2 us against 11.1 for the 64 x 64
+  // tile, 64 rows 13.2 against 11.1; 12288 columns, 16 rows: 13.3 against 11.1).
+  const int64_t groups = int64_t(p.S) * ((p.Ns + 15) / 16);
+  if (p.M <= 16 && groups * 2 <= cus * 3) return rows_of<1, 1, 8, 2, false>(p, st);
+  if (p.M <= 64 && groups * ((p.M + 31) / 32) * 2 <= cus * 3) return rows_of<2, 1, 8, 1, false>(p, st);
+  auto rounds = [&](int bm, int bn, int64_t at_once) {
+    const int64_t tiles = (p.M + bm - 1) / bm * p.S * ((p.Ns + bn - 1) / bn);
+    return (tiles + at_once - 1) / at_once;
+  };
+  const int64_t r0 = rounds(64, 64, cus);
+  const int64_t cost[5] = {r0 == 1 ? 35 : 50 * rounds(64, 64, 2 * cus), 46 * rounds(64, 128, cus),
+                           65 * rounds(128, 128, cus), 98 * rounds(128, 256, cus),
+                           175 * rounds(256, 256, cus)};
+  switch (std::min_element(cost, cost + 5) - cost) {
+    case 0: return tile_launch<2, 2, 2, 2, 4, false>(p, st);
+    case 1: return tile_launch<2, 4, 2, 2, 4, false>(p, st);
+    case 2: return tile_launch<2, 4, 4, 2, 4, false>(p, st);
+    case 3: return tile_launch<2, 4, 4, 4, 3, false>(p, st);
+    default: return tile_launch<2, 4, 8, 4, 2, false>(p, st);
+  }
 }
 
+// Up to six rows an expert the weights' stream is all there is, and 32 columns
+// a workgroup, straight from memory, run it fastest (128 experts of 2880 x
+// 2880: 4 rows each 189 us against 209 for the 128 x 256 tile, 8 rows 224
+// against 216).  Above 256 rows an expert the larger tile moves less.
 hipError_t launch_fp8_moe_gemm(GemmParams p, hipStream_t st) {
-  if (p.block_m == 16) return rows_of<1, 2, 8, 1, true>(p, st);
-  if (p.block_m == 32) return rows_of<2, 2, 8, 1, true>(p, st);
-  if (p.block_m == 64) return tile_launch<1, 4, 4, 2, 3, true>(p, st);
-  return tile_launch<2, 4, 4, 4, 3, true>(p, st);
+  if (p.numel <= 6 * int64_t(p.E)) return rows_of<1, 2, 8, 1, true>(p, st);
+  if (p.numel <= 256 * int64_t(p.E)) return tile_launch<2, 4, 4, 4, 3, true>(p, st);
+  return tile_launch<2, 4, 8, 4, 2, true>(p, st);
 }
 
 }  // namespace mlr
