@@ -108,7 +108,7 @@ int moe_lora_fp8_moe_gemm(const uint8_t* x, const float* x_scales, int32_t x_per
     return MOE_LORA_ERR_INVALID;
   const int64_t numel = M * topk, rows = x_per_pair ? numel : M;
   const int64_t blocks = max_total_blocks(numel, E, block_m);
-  if (rows * K > kInt32Max || rows * p.KB > kInt32Max / 4 || !grid_fits(blocks, S, Ns))
+  if (rows * K > kInt32Max || rows * p.KB > kInt32Max / 4 || !grid_fits(blocks * (block_m / 16), S, Ns))
     return MOE_LORA_ERR_UNSUPPORTED;
   if (numel == 0) return MOE_LORA_OK;
   if (!x || !x_scales || !w || !w_scales || !sorted_token_ids || !expert_ids ||

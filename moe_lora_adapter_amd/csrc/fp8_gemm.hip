@@ -318,8 +318,9 @@ struct Tile {
   static constexpr int XI = BM / 8 / NW, WI = BN / 8 / NW;  // 1 KiB loads a wavefront and stage
   static constexpr int kLoads = XI + WI + 1;
   static constexpr int kX = 0, kW = BM * 128, kS = kW + BN * 128, kStage = kS + BM * 4 + 256;
-  // tiles the loads run ahead by, and this one: their rows' pairs and weights
-  static constexpr int kPairs = NS * kStage, kRing = NS + 1, kList = kPairs + kRing * BM * 8;
+  // the rows' pairs and weights of the tile being stored, of those whose stages
+  // are in the ring (one each where K is one block), and of the next to load
+  static constexpr int kPairs = NS * kStage, kRing = NS + 2, kList = kPairs + kRing * BM * 8;
   static constexpr int lds_bytes(bool grouped) {
     return grouped ? kList + int(sizeof(TileList)) : kPairs;
   }
@@ -337,6 +338,8 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     fp8_gemm_tile_kernel(GemmParams p, int ntiles) {
   using T = Tile<WM, WN, FM, FN, NS>;
   constexpr int BM = T::BM, BN = T::BN, XI = T::XI, WI = T::WI, kLoads = T::kLoads;
+  // whether the columns' loads run ahead of the rows' (below)
+  constexpr bool kEarly = FM > 2;
   constexpr int kX = T::kX, kW = T::kW, kS = T::kS, kStage = T::kStage;
   __shared__ __align__(1024) uint8_t lds[T::lds_bytes(GROUPED)];
 
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   // grouped rows lie anywhere: lane i keeps the offset of this wavefront's row
   // i.  The columns' chunk order has two forms, by bit 3 of the column.
   const int xc = 16 * (cl ^ rl), wc = 16 * (cl ^ swizzle(rl));
-  uint32_t xoff, woff, soff;
+  uint32_t xoff, woff, woff1, soff;
   constexpr int kSegs = BM / kWave, kCols = (BN + kScaleBlock - 1) / kScaleBlock;
   const int sdst = kS + 256 * std::min(w, kSegs);
   const uint32_t sstride = w < kSegs ? uint32_t(p.rows) * 4 : 4;
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   int2* pairs = reinterpret_cast<int2*>(lds + T::kPairs);
 
   auto set_tile = [&]() {
-    uint32_t nx = kOob, nw = kOob, ns = kOob;  // nothing left: loads from nowhere
+    uint32_t nx = kOob, nw = kOob, nw1 = kOob, ns = kOob;  // nothing left: loads from nowhere
     if (lt < items.end) {
       // not to be computed once and kept: the registers are needed
       int ln = lane;
@@ -410,9 +413,11 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
         const RowMap m = row_at(8 * w * XI + ln % (8 * XI));
         if (m.x_row >= 0) nx = uint32_t(m.x_row * p.K);
       } else {
-        nx = uint32_t(8 * w * XI + (ln >> 3)) * uint32_t(p.K);
+        nx = uint32_t(8 * w * XI + (ln >> 3)) * uint32_t(p.K) + xc;
       }
       nw = uint32_t(n0 + 8 * w * WI + (ln >> 3)) * uint32_t(p.K);
+      nw1 = nw + (wc ^ 64);
+      nw += wc;
       // The stage's scales: the first wavefronts load those of 64 rows each,
       // the others (all alike) those of the tile's column blocks.
       const float* from = w < kSegs ? p.xs + x0 : p.ws + mat * p.NB * p.KB;
@@ -432,24 +437,25 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     }
     xoff = nx;
     woff = nw;
+    woff1 = nw1;
     soff = ns;
   };
   // One of a stage's loads.  Chunks past K in a short last block read as
   // zeros; behind the last tile everything does, so that every stage counts the
-  // same loads.  (An offset stays below 2 GiB until kOob's bit is set in it.)
+  // same loads.
   auto load = [&](int l) {
     const uint32_t st = base + uint32_t(lstage) * kStage;
     const int have = p.K - lkb * kScaleBlock;
     const uint32_t k = uint32_t(lkb) * kScaleBlock;
     if (l < XI) {
-      const uint32_t o = GROUPED ? __builtin_amdgcn_ds_bpermute(4 * (8 * l + rl), xoff)
+      const uint32_t o = GROUPED ? __builtin_amdgcn_ds_bpermute(4 * (8 * l + rl), xoff) + xc
                                  : xoff + uint32_t(l) * step8;
-      tile_dma16(xr, st + kX + 1024 * (w * XI + l), (o + xc) | (xc < have ? 0 : kOob), k);
+      tile_dma16(xr, st + kX + 1024 * (w * XI + l), xc < have ? o : kOob, k);
     } else if (l < XI + WI) {
       const int i = l - XI;
-      const int c = wc ^ (16 * swizzle(8 * (w * WI + i)));
+      const int flip = 16 * swizzle(8 * (w * WI + i));
       tile_dma16(wr, st + kW + 1024 * (w * WI + i),
-                 (woff + uint32_t(i) * step8 + c) | (c < have ? 0 : kOob), k);
+                 (wc ^ flip) < have ? (flip ? woff1 : woff) + uint32_t(i) * step8 : kOob, k);
     } else {
       tile_dma4(sr, st + sdst, soff, uint32_t(lkb) * sstride);
     }
@@ -482,8 +488,12 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   // result's multiply-adds run FN MFMAs after it.  The loop's one barrier
   // stands before the last step, once every wavefront has its last rows of the
   // stage in registers; behind it the stage's buffer is refilled, and each
-  // column operand is replaced by the next stage's after its last use.  The
-  // scheduling barriers keep the compiler from undoing this order.
+  // column operand is replaced by the next stage's after its last use.  With
+  // more than two steps a second barrier, behind the first step, says that
+  // every wavefront has the stage's columns in registers, and their buffer is
+  // refilled from there on (4096 x 4096 x 12288: 190 us without, 187 with;
+  // 8192^3 478 and 467).  The scheduling barriers keep the compiler from undoing
+  // this order.
   i32x8_t wf[FN], xf[2];
   float sx[2], sd = 0.0f, sw;
   f32x4_t d[FN];
@@ -530,11 +540,16 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const float s = sx[i & 1] * sw;
+        if (kEarly && i == 1) asm volatile("s_barrier" ::: "memory");
         if (i < FM - 1) {
           rows(st, i + 1);
         } else {
-          ring_barrier<(NS - 2) * kLoads, FM * FN / 2>(__builtin_amdgcn_readfirstlane(young));
-          young = std::max(young - 1, 0);
+          if constexpr (kEarly) {
+            ring_barrier<(NS - 2) * kLoads + WI, FM * FN / 2>(__builtin_amdgcn_readfirstlane(young));
+            young = std::max(young - 1, 0);
+          } else {
+            stage_barrier<(NS - 2) * kLoads>();
+          }
           rows(nx, 0);
           sw = *reinterpret_cast<const float*>(nx + so);
         }
@@ -545,7 +560,14 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
           if (i == FM - 1) {
             columns(nx, f);
 #pragma unroll
-            for (int l = kLoads * f / FN; l < kLoads * (f + 1) / FN; ++l) load(l);
+            for (int l = kLoads * f / FN; l < kLoads * (f + 1) / FN; ++l)
+              if (!kEarly || l < XI || l == kLoads - 1) load(l);
+          }
+          if (kEarly && i >= 1 && i < FM - 1) {
+            constexpr int kSlots = kEarly ? (FM - 2) * FN : 1;
+            const int slot = (i - 1) * FN + f;
+#pragma unroll
+            for (int l = WI * slot / kSlots; l < WI * (slot + 1) / kSlots; ++l) load(XI + l);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -566,7 +588,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     items.at(ct, &row, &tile);
     const int slice = tile / ntiles;
     const int nl = (tile % ntiles) * BN + wn * FN * 16 + 8 * g;  // this lane's columns: 8 of each 32
-    int stores = 0;
+    int stores = 0;  // of this wavefront
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       int64_t y;
@@ -620,11 +642,16 @@ hipError_t tile_launch(GemmParams p, hipStream_t st) {
   return hipSuccess;
 }
 
+template <int MT, int NT, bool GROUPED>
+int64_t rows_grid(const GemmParams& p) {
+  const int64_t pieces = GROUPED ? int64_t(p.blocks) * p.block_m / (16 * MT) : (p.M + 16 * MT - 1) / (16 * MT);
+  return pieces * p.S * ((p.Ns + 16 * NT - 1) / (16 * NT));
+}
+
 template <int MT, int NT, int KW, int U, bool GROUPED>
 hipError_t rows_of(const GemmParams& p, hipStream_t st) {
   const int ntiles = (p.Ns + 16 * NT - 1) / (16 * NT);
-  const int64_t pieces = GROUPED ? int64_t(p.blocks) * p.block_m / (16 * MT) : (p.M + 16 * MT - 1) / (16 * MT);
-  const int64_t grid = pieces * p.S * ntiles;
+  const int64_t grid = rows_grid<MT, NT, GROUPED>(p);
   hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, NT, KW, U, GROUPED>), dim3(unsigned(grid)),
                      dim3(KW * kWave), 0, st, p, ntiles);
   return hipGetLastError();
@@ -634,7 +661,7 @@ hipError_t rows_of(const GemmParams& p, hipStream_t st) {
 
 // The tile whose rounds over the device cost least.  A round's time for each
 // 128 of K, in hundredths of a microsecond (measured at K = 4096 with every
-// CU busy): 64 x 64 35, or 50 with two on a CU; 64 x 128 46; 128 x 128 65;
+// CU busy): 64 x 64 36, or 50 with two on a CU; 64 x 128 43; 128 x 128 63;
 // 128 x 256 98; 256 x 256 175.
 hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
   const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
@@ -649,14 +676,14 @@ hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
     return (tiles + at_once - 1) / at_once;
   };
   const int64_t r0 = rounds(64, 64, cus);
-  const int64_t cost[5] = {r0 == 1 ? 35 : 50 * rounds(64, 64, 2 * cus), 46 * rounds(64, 128, cus),
-                           65 * rounds(128, 128, cus), 98 * rounds(128, 256, cus),
+  const int64_t cost[5] = {r0 == 1 ? 36 : 50 * rounds(64, 64, 2 * cus), 43 * rounds(64, 128, cus),
+                           63 * rounds(128, 128, cus), 98 * rounds(128, 256, cus),
                            175 * rounds(256, 256, cus)};
   switch (std::min_element(cost, cost + 5) - cost) {
     case 0: return tile_launch<2, 2, 2, 2, 4, false>(p, st);
     case 1: return tile_launch<2, 4, 2, 2, 4, false>(p, st);
-    case 2: return tile_launch<2, 4, 4, 2, 4, false>(p, st);
-    case 3: return tile_launch<2, 4, 4, 4, 3, false>(p, st);
+    case 2: return tile_launch<2, 4, 4, 2, 2, false>(p, st);
+    case 3: return tile_launch<2, 4, 4, 4, 2, false>(p, st);
     default: return tile_launch<2, 4, 8, 4, 2, false>(p, st);
   }
 }
@@ -664,10 +691,15 @@ hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
 // Up to six rows an expert the weights' stream is all there is, and 32 columns
 // a workgroup, straight from memory, run it fastest (128 experts of 2880 x
 // 2880: 4 rows each 189 us against 209 for the 128 x 256 tile, 8 rows 224
-// against 216).  Above 256 rows an expert the larger tile moves less.
+// against 216).  Above 128 rows an expert the larger tile reads the weights
+// less often (64 rows: 259 us against 309 for 256 x 256; with skewed routing and
+// 1536 x 2048, 128 rows 119 against 135, 256 rows 173 against 176, 512 rows 284
+// against 277).
 hipError_t launch_fp8_moe_gemm(GemmParams p, hipStream_t st) {
-  if (p.numel <= 6 * int64_t(p.E)) return rows_of<1, 2, 8, 1, true>(p, st);
-  if (p.numel <= 256 * int64_t(p.E)) return tile_launch<2, 4, 4, 4, 3, true>(p, st);
+  // (a launch has fewer than 2^32 threads)
+  const bool fits = rows_grid<1, 2, true>(p) < (int64_t(1) << 32) / (8 * kWave);
+  if (p.numel <= 6 * int64_t(p.E) && fits) return rows_of<1, 2, 8, 1, true>(p, st);
+  if (p.numel <= 128 * int64_t(p.E)) return tile_launch<2, 4, 4, 4, 2, true>(p, st);
   return tile_launch<2, 4, 8, 4, 2, true>(p, st);
 }
 

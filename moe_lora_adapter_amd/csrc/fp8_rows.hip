@@ -79,7 +79,8 @@ __device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
 template <int T, int CH, bool RES>
 __global__ void __launch_bounds__(T) rms_norm_fp8_kernel(NormParams p) {
   __shared__ float part[T / kWave];
-  const int64_t row = blockIdx.x;
+  const int64_t row = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+  if (row >= p.M) return;
   const int nc = p.H / 8;
   const uint4* x = reinterpret_cast<const uint4*>(p.x + row * p.H);
   float v[CH][8];
@@ -167,7 +168,9 @@ __global__ void __launch_bounds__(kTS) silu_mul_fp8_kernel(SiluParams p, int32_t
 
 template <int T, int CH>
 hipError_t norm_of(const NormParams& p, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(p.M));
+  // a launch has fewer than 2^32 threads along one axis
+  const int64_t most = (int64_t(1) << 32) / T - 1, y = (p.M + most - 1) / most;
+  const dim3 grid(unsigned((p.M + y - 1) / y), unsigned(y));
   if (p.residual)
     hipLaunchKernelGGL((rms_norm_fp8_kernel<T, CH, true>), grid, dim3(T), 0, st, p);
   else

@@ -143,6 +143,37 @@ def test_gemm_whole_numbers_exactly(M, K, Ns, S):
     assert torch.equal(y, ref.float().to(BF))
 
 
+# More tiles than the device holds at once, so that a workgroup takes several: each tile size, K of
+# one block, of two and of more than the ring's stages, tiles that end in the last row and column.
+MANY = [(4100, 64, 5000, 1), (4100, 144, 4104, 1), (5000, 400, 4304, 2), (3000, 272, 9000, 1),
+        (4096, 1040, 8200, 1), (2000, 528, 4104, 1), (700, 400, 4200, 2), (1500, 128, 12304, 1),
+        (65, 272, 40000, 1), (130, 656, 33000, 1), (64, 272, 70000, 1), (12000, 272, 264, 1),
+        (40000, 144, 72, 1)]
+
+
+def _wide(q, s):
+    return q.float() * s.t().repeat_interleave(128, 1)[:, :q.shape[1]]
+
+
+def _wide_w(q, s):
+    s = s.repeat_interleave(128, -2)[..., :q.shape[-2], :]
+    return q.float() * s.repeat_interleave(128, -1)[..., :q.shape[-1]]
+
+
+@pytest.mark.parametrize("M,K,Ns,S", MANY)
+def test_gemm_many_tiles_exactly(M, K, Ns, S):
+    """Whole numbers again, where any order of fp32 additions is exact: torch's product on the GPU."""
+    g = gen(M + Ns)
+    xq, xs = fr.whole_rows(g, M, K)
+    wq, ws = fr.whole_weights(g, S, Ns, K)
+    x, w, sc = _rows(xq, xs), wq.to(DEV), ws.to(DEV)
+    buf = torch.full((M * S * Ns + 65536,), 3.0, dtype=BF, device=DEV)
+    y = mla.moe_lora_fp8_gemm(x, w, sc, buf[:M * S * Ns].view(M, S * Ns))
+    want = (_wide(x.q, x.scales) @ _wide_w(w, sc).view(S * Ns, K).t().contiguous()).to(BF)
+    assert torch.equal(y, want)
+    assert bool((buf[M * S * Ns:] == 3.0).all())
+
+
 @pytest.mark.parametrize("M", [3, 200, 700])
 def test_gemm_nan_stays_in_its_row_and_column(M):
     xq, xs, wq, ws = _gemm(M, 656, 264, 1, M)
@@ -259,6 +290,40 @@ def test_moe_gemm_whole_numbers_exactly(case):
         ref, _ = fr.gemm(xq.view(torch.uint8)[r].view(fr.F8), xs[:, r], wq[e], ws[e])
         want[p] = ((ref * tw.view(-1)[p].to(D)[:, None]) if mul else ref).float().to(BF)
     assert torch.equal(y.cpu().view(-1, S * Ns), want)
+
+
+@pytest.mark.parametrize("M,topk,K,Ns,S,E,B,kind", [
+    (3000, 4, 272, 392, 2, 16, 16, "invalid"), (3000, 2, 144, 2200, 1, 40, 64, "uniform"),
+    (9000, 4, 64, 520, 1, 40, 128, "uniform"), (6000, 4, 400, 136, 2, 64, 32, "invalid"),
+    (2500, 8, 272, 1032, 1, 128, 128, "uniform"), (140000, 2, 16, 8, 1, 3, 16, "invalid"),
+    (150000, 2, 48, 24, 1, 600, 16, "uniform")])
+def test_moe_gemm_many_tiles_exactly(M, topk, K, Ns, S, E, B, kind):
+    """Tiles of several align blocks, more of them than the device holds at once; the last two have
+    more blocks than one launch takes."""
+    ids = _routing(np.random.default_rng(M + E), M, topk, E, kind)
+    g = gen(M + topk)
+    xq, xs = fr.whole_rows(g, M, K)
+    wq, ws = fr.whole_weights(g, E, S, Ns, K)
+    tw = 2.0 ** torch.randint(-2, 3, (M, topk), generator=g).float()
+    x, w, sc, dw = _rows(xq, xs), wq.to(DEV), ws.to(DEV), tw.to(DEV)
+    y = torch.full((M, topk, S * Ns), 5.0, dtype=BF, device=DEV)
+    mla.moe_lora_fp8_moe_gemm(x, w, sc, _base_align(ids, E, B), dw, y, mul_routed_weight=True)
+    xw, want = _wide(x.q, x.scales), torch.full((M * topk, S * Ns), 5.0, dtype=BF, device=DEV)
+    flat, wt = gh.i32_dev(ids).view(-1), dw.view(-1)
+    for e in range(E):
+        p = (flat == e).nonzero().view(-1)
+        d = xw[p // topk] @ _wide_w(w[e], sc[e]).view(S * Ns, K).t().contiguous()
+        want[p] = (d * wt[p][:, None]).to(BF)
+    assert torch.equal(y.view(M * topk, S * Ns), want)
+
+
+def test_rms_norm_more_rows_than_a_grid_axis():
+    M, H = (1 << 26) + 5, 8
+    x = torch.ones((M, H), dtype=BF, device=DEV)
+    x[-1] = 2.0
+    out = mla.moe_lora_rms_norm_fp8(x, torch.ones(H, dtype=BF, device=DEV), eps=0.0)
+    assert bool((out.q.view(torch.uint8) == 0x7e).all())  # 448, the largest of its block
+    assert bool(((out.scales - 1 / 448).abs() < 1e-8).all())
 
 
 @pytest.mark.parametrize("B", [16, 64, 128])
