@@ -454,116 +454,159 @@ def _refuse(t, name, dtype, device, shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _launch(fn, name, device, stream, *args):
-    """Call an entry point on `device`: its stream last, that device current."""
+def _call(name, x, stream, *args):
+    """Call an entry point on x's device: its stream last, that device current."""
     import torch
-    index = device.index
-    if index is None or device.type != "cuda":
+    device = x.device
+    if device.type != "cuda":
         raise ValueError(f"{name} needs tensors on a GPU, got {device}")
     if stream is not None and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, expected {device}")
-    # the raw handles: a Stream object costs more than the rest of the call
-    if torch._C._cuda_getDevice() != index:
-        with torch.cuda.device(device):
-            return _launch(fn, name, device, stream, *args)
-    rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    with torch.cuda.device(device):
+        raw = torch.cuda.current_stream() if stream is None else stream
+        rc = getattr(lib(), name)(*args, raw.cuda_stream)
     if rc != OK:
         raise MoeLoraError(rc, name)
 
+
+def _direct(torch, device, stream):
+    """The raw current stream when nothing has to be switched for a call on `device`, else None:
+    making a Stream object costs more than the call."""
+    if stream is None and device >= 0 and torch._C._cuda_getDevice() == device:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return None
+
+
+# The checks below are written out, attribute by attribute: in a serving loop's small calls a
+# helper per tensor costs as much as the launch.
 
 def moe_lora_rms_norm_fp8(x, weight, *, eps: float = 1e-6, residual=None, residual_out=None, y=None,
                           out: Fp8Rows | None = None, stream=None) -> Fp8Rows:
     """RMS norm of x (+ residual) as 8-bit rows, and as bf16 in y when given; the sum goes to
     residual_out (None: in place on residual); see moe_lora.h."""
     import torch
-    bf, dev = torch.bfloat16, x.device
-    _check(x, "x", bf, dev)
-    if x.dim() != 2:
+    bf = torch.bfloat16
+    if not isinstance(x, torch.Tensor) or x.dtype is not bf or not x.is_contiguous():
+        _check(x, "x", bf, x.device)
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [M, H]")
-    shape = M, H = x.shape
+    M, H = shape
+    at = x.get_device()
     if out is None:
-        out = alloc_fp8_rows(M, H, dev)
-    q, scales = out.q, out.scales
-    ptr = [x.data_ptr(), None, None, None]
-    if residual is not None and residual_out is None:
-        residual_out = residual
-    elif residual is None and residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    for i, t, name in ((1, residual, "residual"), (2, residual_out, "residual_out"), (3, y, "y")):
-        if t is not None:
-            if t.dtype is not bf or t.shape != shape or not t.is_contiguous() or t.device != dev:
-                _refuse(t, name, bf, dev, shape)
-            ptr[i] = t.data_ptr()
+        out = alloc_fp8_rows(M, H, x.device)
     if (weight.dtype is not bf or weight.shape != (H,) or not weight.is_contiguous()
-            or weight.device != dev):
-        _refuse(weight, "weight", bf, dev, (H,))
-    _check_rows(q, scales, "out", M, H, dev)
-    _launch(lib().moe_lora_rms_norm_fp8, "moe_lora_rms_norm_fp8", dev, stream, ptr[0], ptr[1],
-            weight.data_ptr(), M, H, eps, ptr[2], ptr[3], q.data_ptr(), scales.data_ptr())
+            or weight.get_device() != at):
+        _refuse(weight, "weight", bf, x.device, (H,))
+    pr = po = py = None
+    if residual is not None:
+        if (residual.dtype is not bf or residual.shape != shape or not residual.is_contiguous()
+                or residual.get_device() != at):
+            _refuse(residual, "residual", bf, x.device, shape)
+        pr = po = residual.data_ptr()
+        if residual_out is not None:
+            if (residual_out.dtype is not bf or residual_out.shape != shape
+                    or not residual_out.is_contiguous() or residual_out.get_device() != at):
+                _refuse(residual_out, "residual_out", bf, x.device, shape)
+            po = residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if y is not None:
+        if (y.dtype is not bf or y.shape != shape or not y.is_contiguous()
+                or y.get_device() != at):
+            _refuse(y, "y", bf, x.device, shape)
+        py = y.data_ptr()
+    pq, ps = _rows_ptrs(torch, out, "out", M, H, x, at)
+    raw = _direct(torch, at, stream)
+    if raw is None:
+        _call("moe_lora_rms_norm_fp8", x, stream, x.data_ptr(), pr, weight.data_ptr(), M, H, eps,
+              po, py, pq, ps)
+        return out
+    rc = lib().moe_lora_rms_norm_fp8(x.data_ptr(), pr, weight.data_ptr(), M, H, eps, po, py, pq,
+                                     ps, raw)
+    if rc != OK:
+        raise MoeLoraError(rc, "moe_lora_rms_norm_fp8")
     return out
 
 
-def _check_rows(q, scales, name, M, K, dev):
-    import torch
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    if q.dtype is not f8 or q.shape != (M, K) or not q.is_contiguous() or q.device != dev:
-        _refuse(q, name + ".q", f8, dev, (M, K))
+def _rows_ptrs(torch, rows, name, M, K, like, at):
+    """Checks 8-bit rows [M, K] on the device of `like`; their two addresses."""
+    q, s = rows.q, rows.scales
+    if (q.dtype is not torch.float8_e4m3fn or q.shape != (M, K) or not q.is_contiguous()
+            or q.get_device() != at):
+        _refuse(q, name + ".q", torch.float8_e4m3fn, like.device, (M, K))
     kb = -(-K // FP8_BLOCK)
-    if (scales.dtype is not f32 or scales.shape != (kb, M) or not scales.is_contiguous()
-            or scales.device != dev):
-        _refuse(scales, name + ".scales", f32, dev, (kb, M))
+    if (s.dtype is not torch.float32 or s.shape != (kb, M) or not s.is_contiguous()
+            or s.get_device() != at):
+        _refuse(s, name + ".scales", torch.float32, like.device, (kb, M))
+    return q.data_ptr(), s.data_ptr()
 
 
 def moe_lora_silu_mul_fp8(y, *, h=None, out: Fp8Rows | None = None, stream=None) -> Fp8Rows:
     """silu(gate) * up of y = [..., gate | up] as 8-bit rows, and as bf16 in h when given; see
     moe_lora.h."""
     import torch
-    dev = y.device
-    _check(y, "y", torch.bfloat16, dev)
-    if y.dim() < 2 or y.shape[-1] % 2:
+    bf = torch.bfloat16
+    if not isinstance(y, torch.Tensor) or y.dtype is not bf or not y.is_contiguous():
+        _check(y, "y", bf, y.device)
+    shape = y.shape
+    if len(shape) < 2 or shape[-1] % 2:
         raise ValueError("y must be [..., 2 * I]")
-    I = y.shape[-1] // 2
-    P = y.numel() // max(1, 2 * I)
-    if h is not None and (h.dtype is not torch.bfloat16 or h.shape != (P, I)
-                          or not h.is_contiguous() or h.device != dev):
-        _refuse(h, "h", torch.bfloat16, dev, (P, I))
+    I = shape[-1] // 2
+    P = y.numel() // (2 * I) if I else 0
+    at, ph = y.get_device(), None
+    if h is not None:
+        if (h.dtype is not bf or h.shape != (P, I) or not h.is_contiguous()
+                or h.get_device() != at):
+            _refuse(h, "h", bf, y.device, (P, I))
+        ph = h.data_ptr()
     if out is None:
-        out = alloc_fp8_rows(P, I, dev)
-    q, scales = out.q, out.scales
-    _check_rows(q, scales, "out", P, I, dev)
-    _launch(lib().moe_lora_silu_mul_fp8, "moe_lora_silu_mul_fp8", dev, stream, y.data_ptr(), P, I,
-            None if h is None else h.data_ptr(), q.data_ptr(), scales.data_ptr())
+        out = alloc_fp8_rows(P, I, y.device)
+    pq, ps = _rows_ptrs(torch, out, "out", P, I, y, at)
+    raw = _direct(torch, at, stream)
+    if raw is None:
+        _call("moe_lora_silu_mul_fp8", y, stream, y.data_ptr(), P, I, ph, pq, ps)
+        return out
+    rc = lib().moe_lora_silu_mul_fp8(y.data_ptr(), P, I, ph, pq, ps, raw)
+    if rc != OK:
+        raise MoeLoraError(rc, "moe_lora_silu_mul_fp8")
     return out
 
 
-def _check_weights(w, w_scales, dev):
-    import torch
-    _check(w, "w", torch.float8_e4m3fn, dev)
-    *lead, Ns, K = w.shape
-    shape = (*lead, -(-Ns // FP8_BLOCK), -(-K // FP8_BLOCK))
-    if (w_scales.dtype is not torch.float32 or w_scales.shape != shape
-            or not w_scales.is_contiguous() or w_scales.device != dev):
-        _refuse(w_scales, "w_scales", torch.float32, dev, shape)
+def _weight_ptrs(torch, w, w_scales, shape, at):
+    """Checks 8-bit weights [..., Ns, K] and their scales; their two addresses."""
+    if w.dtype is not torch.float8_e4m3fn or not w.is_contiguous():
+        _check(w, "w", torch.float8_e4m3fn, w.device)
+    want = (*shape[:-2], -(-shape[-2] // FP8_BLOCK), -(-shape[-1] // FP8_BLOCK))
+    if (w_scales.dtype is not torch.float32 or w_scales.shape != want
+            or not w_scales.is_contiguous() or w_scales.get_device() != at):
+        _refuse(w_scales, "w_scales", torch.float32, w.device, want)
+    return w.data_ptr(), w_scales.data_ptr()
 
 
 def moe_lora_fp8_gemm(x: Fp8Rows, w, w_scales, y=None, *, stream=None):
     """8-bit rows times w [S, Ns, K] (e4m3, a scale per 128 x 128 block of a slice); y bf16
     [M, S*Ns] is allocated when not given; see moe_lora.h."""
     import torch
-    dev, xq, xs = w.device, x.q, x.scales
-    if w.dim() != 3 or xq.dim() != 2:
+    shape, at = w.shape, w.get_device()
+    if len(shape) != 3 or x.q.dim() != 2:
         raise ValueError("w must be [S, Ns, K] and x.q [M, K]")
-    S, Ns, K = w.shape
-    M = xq.shape[0]
-    _check_weights(w, w_scales, dev)
-    _check_rows(xq, xs, "x", M, K, dev)
+    S, Ns, K = shape
+    M = x.q.shape[0]
+    pw, pws = _weight_ptrs(torch, w, w_scales, shape, at)
+    pq, ps = _rows_ptrs(torch, x, "x", M, K, w, at)
     if y is None:
-        y = torch.empty((M, S * Ns), dtype=torch.bfloat16, device=dev)
+        y = torch.empty((M, S * Ns), dtype=torch.bfloat16, device=w.device)
     elif (y.dtype is not torch.bfloat16 or y.shape != (M, S * Ns) or not y.is_contiguous()
-          or y.device != dev):
-        _refuse(y, "y", torch.bfloat16, dev, (M, S * Ns))
-    _launch(lib().moe_lora_fp8_gemm, "moe_lora_fp8_gemm", dev, stream, xq.data_ptr(), xs.data_ptr(),
-            w.data_ptr(), w_scales.data_ptr(), M, K, Ns, S, y.data_ptr())
+          or y.get_device() != at):
+        _refuse(y, "y", torch.bfloat16, w.device, (M, S * Ns))
+    raw = _direct(torch, at, stream)
+    if raw is None:
+        _call("moe_lora_fp8_gemm", w, stream, pq, ps, pw, pws, M, K, Ns, S, y.data_ptr())
+        return y
+    rc = lib().moe_lora_fp8_gemm(pq, ps, pw, pws, M, K, Ns, S, y.data_ptr(), raw)
+    if rc != OK:
+        raise MoeLoraError(rc, "moe_lora_fp8_gemm")
     return y
 
 
@@ -572,32 +615,39 @@ def moe_lora_fp8_moe_gemm(x: Fp8Rows, w, w_scales, align: AlignOutput, topk_weig
     """8-bit rows times each routed pair's expert of w [E, S, Ns, K], into y [M, topk, S*Ns]; align
     is one slot's (L = 1); see moe_lora.h."""
     import torch
-    i32, dev, xq, xs = torch.int32, y.device, x.q, x.scales
-    _check(y, "y", torch.bfloat16, dev)
-    if w.dim() != 4 or y.dim() != 3 or xq.dim() != 2:
+    i32, shape, at = torch.int32, w.shape, w.get_device()
+    if len(shape) != 4 or y.dim() != 3 or x.q.dim() != 2:
         raise ValueError("w must be [E, S, Ns, K], y [M, topk, S*Ns] and x.q [rows, K]")
-    E, S, Ns, K = w.shape
+    E, S, Ns, K = shape
     M, topk, N = y.shape
     if N != S * Ns:
         raise ValueError("y's last dim must be S*Ns")
-    _check_weights(w, w_scales, dev)
-    _check_rows(xq, xs, "x", M * topk if x_per_pair else M, K, dev)
-    tw = None
+    if y.dtype is not torch.bfloat16 or not y.is_contiguous() or y.get_device() != at:
+        _check(y, "y", torch.bfloat16, w.device)
+    pw, pws = _weight_ptrs(torch, w, w_scales, shape, at)
+    pq, ps = _rows_ptrs(torch, x, "x", M * topk if x_per_pair else M, K, w, at)
+    ptw = None
     if topk_weights is not None:
         if (topk_weights.dtype is not torch.float32 or topk_weights.shape != (M, topk)
-                or not topk_weights.is_contiguous() or topk_weights.device != dev):
-            _refuse(topk_weights, "topk_weights", torch.float32, dev, (M, topk))
-        tw = topk_weights.data_ptr()
+                or not topk_weights.is_contiguous() or topk_weights.get_device() != at):
+            _refuse(topk_weights, "topk_weights", torch.float32, w.device, (M, topk))
+        ptw = topk_weights.data_ptr()
     block_m = align.block_m
     cap = align_capacity(M, topk, E, block_m)
     ids, eids, ntpp = align.sorted_token_ids, align.expert_ids, align.num_tokens_post_padded
-    for t, name, shape in ((ids, "sorted_token_ids", (1, cap)),
-                           (eids, "expert_ids", (1, cap // block_m)),
-                           (ntpp, "num_tokens_post_padded", (1,))):
-        if t.dtype is not i32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
-            _refuse(t, "align." + name, i32, dev, shape)
-    _launch(lib().moe_lora_fp8_moe_gemm, "moe_lora_fp8_moe_gemm", dev, stream, xq.data_ptr(),
-            xs.data_ptr(), 1 if x_per_pair else 0, w.data_ptr(), w_scales.data_ptr(),
-            ids.data_ptr(), eids.data_ptr(), ntpp.data_ptr(), tw, 1 if mul_routed_weight else 0,
-            M, topk, K, Ns, S, E, block_m, y.data_ptr())
+    for t, name, want in ((ids, "sorted_token_ids", (1, cap)),
+                          (eids, "expert_ids", (1, cap // block_m)),
+                          (ntpp, "num_tokens_post_padded", (1,))):
+        if t.dtype is not i32 or t.shape != want or not t.is_contiguous() or t.get_device() != at:
+            _refuse(t, "align." + name, i32, w.device, want)
+    args = (pq, ps, 1 if x_per_pair else 0, pw, pws, ids.data_ptr(), eids.data_ptr(),
+            ntpp.data_ptr(), ptw, 1 if mul_routed_weight else 0, M, topk, K, Ns, S, E, block_m,
+            y.data_ptr())
+    raw = _direct(torch, at, stream)
+    if raw is None:
+        _call("moe_lora_fp8_moe_gemm", w, stream, *args)
+        return y
+    rc = lib().moe_lora_fp8_moe_gemm(*args, raw)
+    if rc != OK:
+        raise MoeLoraError(rc, "moe_lora_fp8_moe_gemm")
     return y

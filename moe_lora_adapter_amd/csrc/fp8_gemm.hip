@@ -472,45 +472,12 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   };
 
   // ---- the multiplying side
-  f32x4_t acc[FM][FN];
-  auto clear = [&]() {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int f = 0; f < FN; ++f) acc[i][f] = f32x4_t{0, 0, 0, 0};
-  };
   const int xrow = wm * FM * 16 + a, wrow = wn * FN * 16 + 8 * (a >> 2) + (a & 3);
   const int xo = kX + xrow * 128 + 16 * (g ^ (a & 7));
   const int wo = kW + wrow * 128 + 16 * (g ^ (a & 7));
   const int so = kS + BM * 4 + wn * FN * 16 / kScaleBlock * 4;  // this wavefront's column block
+  constexpr int kWait = (NS - 2) * kLoads + (kEarly ? WI : 0);  // younger loads at a stage's barrier
 
-  // A stage is FM steps of FN MFMAs: a step reads the next one's rows, and a
-  // result's multiply-adds run FN MFMAs after it.  The loop's one barrier
-  // stands before the last step, once every wavefront has its last rows of the
-  // stage in registers; behind it the stage's buffer is refilled, and each
-  // column operand is replaced by the next stage's after its last use.  With
-  // more than two steps a second barrier, behind the first step, says that
-  // every wavefront has the stage's columns in registers, and their buffer is
-  // refilled from there on (4096 x 4096 x 12288: 190 us without, 187 with;
-  // 8192^3 478 and 467).  The scheduling barriers keep the compiler from undoing
-  // this order.
-  i32x8_t wf[FN], xf[2];
-  float sx[2], sd = 0.0f, sw;
-  f32x4_t d[FN];
-  auto add = [&](int i, int f) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][f][j] = fmaf(d[f][j], sd, acc[i][f][j]);
-  };
-  auto columns = [&](const uint8_t* st, int f) {
-    const int o = 4096 * (f >> 1) + 512 * (f & 1);
-    wf[f] = join(*reinterpret_cast<const uint4*>(st + wo + o),
-                 *reinterpret_cast<const uint4*>(st + (wo ^ 64) + o));
-  };
-  auto rows = [&](const uint8_t* st, int i) {
-    xf[i & 1] = join(*reinterpret_cast<const uint4*>(st + xo + 2048 * i),
-                     *reinterpret_cast<const uint4*>(st + (xo ^ 64) + 2048 * i));
-    sx[i & 1] = *reinterpret_cast<const float*>(st + kS + 4 * (xrow + 16 * i));
-  };
   set_tile();
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
@@ -520,74 +487,127 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     if (lkb == p.KB) next_loads();
   }
   stage_barrier<(NS - 1) * kLoads>();
-#pragma unroll
-  for (int f = 0; f < FN; ++f) {
-    columns(lds, f);
-    d[f] = f32x4_t{0, 0, 0, 0};
-  }
-  rows(lds, 0);
-  sw = *reinterpret_cast<const float*>(lds + so);
-  clear();
-  int kb = 0, stage = 0, ring = 0;
+  int stage = 0, ring = 0;
   int young = 0;  // stages still waited for whose loads are older than the last tile's stores
-  while (true) {
-    // stages until one side changes its tile
-    const int n = std::min(p.KB - kb, p.KB - lkb);
-    for (int r = 0; r < n; ++r) {
-      const uint8_t* st = lds + stage * kStage;
-      stage = stage + 1 == NS ? 0 : stage + 1;
-      const uint8_t* nx = lds + stage * kStage;
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const float s = sx[i & 1] * sw;
-        if (kEarly && i == 1) asm volatile("s_barrier" ::: "memory");
-        if (i < FM - 1) {
-          rows(st, i + 1);
-        } else {
-          if constexpr (kEarly) {
-            ring_barrier<(NS - 2) * kLoads + WI, FM * FN / 2>(__builtin_amdgcn_readfirstlane(young));
-            young = std::max(young - 1, 0);
-          } else {
-            stage_barrier<(NS - 2) * kLoads>();
-          }
-          rows(nx, 0);
-          sw = *reinterpret_cast<const float*>(nx + so);
-        }
-#pragma unroll
-        for (int f = 0; f < FN; ++f) {
-          add((i + FM - 1) % FM, f);
-          d[f] = mfma_e4m3(wf[f], xf[i & 1]);
-          if (i == FM - 1) {
-            columns(nx, f);
-#pragma unroll
-            for (int l = kLoads * f / FN; l < kLoads * (f + 1) / FN; ++l)
-              if (!kEarly || l < XI || l == kLoads - 1) load(l);
-          }
-          if (kEarly && i >= 1 && i < FM - 1) {
-            constexpr int kSlots = kEarly ? (FM - 2) * FN : 1;
-            const int slot = (i - 1) * FN + f;
-#pragma unroll
-            for (int l = WI * slot / kSlots; l < WI * (slot + 1) / kSlots; ++l) load(XI + l);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        sd = s;
-      }
-      loaded();
-    }
-    kb += n;
-    if (lkb == p.KB) next_loads();
-    if (kb < p.KB) continue;
-    // the tile is done
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      add(FM - 1, f);
-      d[f] = f32x4_t{0, 0, 0, 0};
-    }
+  for (; ct < items.end; ct += items.step, ring = ring + 1 == T::kRing ? 0 : ring + 1) {
     uint32_t row, tile;
     items.at(ct, &row, &tile);
-    const int slice = tile / ntiles;
-    const int nl = (tile % ntiles) * BN + wn * FN * 16 + 8 * g;  // this lane's columns: 8 of each 32
+    const int slice = tile / ntiles, n0 = (tile % ntiles) * BN;
+    // A wavefront without a row or a column of the tile (its rows come first,
+    // what is missing last) only loads and keeps the barriers.
+    bool none = n0 + wn * FN * 16 >= p.Ns;
+    if constexpr (GROUPED) {
+      none |= __builtin_amdgcn_readfirstlane(pairs[ring * BM + wm * FM * 16].x) < 0;
+    } else {
+      none |= int64_t(row) * BM + wm * FM * 16 >= p.M;
+    }
+    if (none) {
+      for (int kb = 0; kb < p.KB; ++kb) {
+        if constexpr (kEarly) {
+          asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+          for (int l = XI; l < XI + WI; ++l) load(l);
+        }
+        stage_barrier<kWait>();
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l)
+          if (!kEarly || l < XI || l == kLoads - 1) load(l);
+        loaded();
+        stage = stage + 1 == NS ? 0 : stage + 1;
+        if (lkb == p.KB) next_loads();
+      }
+      young = 0;
+      continue;
+    }
+
+    // A stage is FM steps of FN MFMAs: a step reads the next one's rows, and a
+    // result's multiply-adds run FN MFMAs after it.  The stage's barrier stands
+    // before the last step, once every wavefront has its last rows of the stage
+    // in registers; behind it the stage's buffer is refilled, and each column
+    // operand is replaced by the next stage's after its last use.  With more
+    // than two steps a second barrier, behind the first step, says that every
+    // wavefront has the stage's columns in registers, and their buffer is
+    // refilled from there on (4096 x 4096 x 12288: 190 us without, 187 with;
+    // 8192^3 478 and 467).  The scheduling barriers keep the compiler from
+    // undoing this order.
+    f32x4_t acc[FM][FN], d[FN];
+    i32x8_t wf[FN], xf[2];
+    float sx[2], sd = 0.0f, sw;
+    auto add = [&](int i, int f) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][f][j] = fmaf(d[f][j], sd, acc[i][f][j]);
+    };
+    auto columns = [&](const uint8_t* st, int f) {
+      const int o = 4096 * (f >> 1) + 512 * (f & 1);
+      wf[f] = join(*reinterpret_cast<const uint4*>(st + wo + o),
+                   *reinterpret_cast<const uint4*>(st + (wo ^ 64) + o));
+    };
+    auto rows = [&](const uint8_t* st, int i) {
+      xf[i & 1] = join(*reinterpret_cast<const uint4*>(st + xo + 2048 * i),
+                       *reinterpret_cast<const uint4*>(st + (xo ^ 64) + 2048 * i));
+      sx[i & 1] = *reinterpret_cast<const float*>(st + kS + 4 * (xrow + 16 * i));
+    };
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      columns(lds + stage * kStage, f);
+      d[f] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < FM; ++i) acc[i][f] = f32x4_t{0, 0, 0, 0};
+    }
+    rows(lds + stage * kStage, 0);
+    sw = *reinterpret_cast<const float*>(lds + stage * kStage + so);
+    for (int kb = 0; kb < p.KB;) {
+      // the stages until the loads change their tile
+      const int n = std::min(p.KB - kb, p.KB - lkb);
+      for (int r = 0; r < n; ++r) {
+        const uint8_t* st = lds + stage * kStage;
+        stage = stage + 1 == NS ? 0 : stage + 1;
+        const uint8_t* nx = lds + stage * kStage;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const float s = sx[i & 1] * sw;
+          if (kEarly && i == 1) asm volatile("s_barrier" ::: "memory");
+          if (i < FM - 1) {
+            rows(st, i + 1);
+          } else {
+            if constexpr (kEarly) {
+              ring_barrier<kWait, FM * FN / 2>(__builtin_amdgcn_readfirstlane(young));
+              young = std::max(young - 1, 0);
+            } else {
+              stage_barrier<kWait>();
+            }
+            rows(nx, 0);
+            sw = *reinterpret_cast<const float*>(nx + so);
+          }
+#pragma unroll
+          for (int f = 0; f < FN; ++f) {
+            add((i + FM - 1) % FM, f);
+            d[f] = mfma_e4m3(wf[f], xf[i & 1]);
+            if (i == FM - 1) {
+              columns(nx, f);
+#pragma unroll
+              for (int l = kLoads * f / FN; l < kLoads * (f + 1) / FN; ++l)
+                if (!kEarly || l < XI || l == kLoads - 1) load(l);
+            }
+            if (kEarly && i >= 1 && i < FM - 1) {
+              constexpr int kSlots = kEarly ? (FM - 2) * FN : 1;
+              const int slot = (i - 1) * FN + f;
+#pragma unroll
+              for (int l = WI * slot / kSlots; l < WI * (slot + 1) / kSlots; ++l) load(XI + l);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          sd = s;
+        }
+        loaded();
+      }
+      kb += n;
+      if (lkb == p.KB) next_loads();
+    }
+#pragma unroll
+    for (int f = 0; f < FN; ++f) add(FM - 1, f);
+
+    const int nl = n0 + wn * FN * 16 + 8 * g;  // this lane's columns: 8 of each 32
     int stores = 0;  // of this wavefront
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -614,11 +634,6 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
       }
     }
     young = stores == FM * FN / 2 ? NS - 1 : 0;
-    ct += items.step;
-    if (ct >= items.end) break;
-    clear();
-    kb = 0;
-    ring = ring + 1 == T::kRing ? 0 : ring + 1;
   }
   // no load into LDS outlives its workgroup
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
@@ -691,15 +706,15 @@ hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
 // Up to six rows an expert the weights' stream is all there is, and 32 columns
 // a workgroup, straight from memory, run it fastest (128 experts of 2880 x
 // 2880: 4 rows each 189 us against 209 for the 128 x 256 tile, 8 rows 224
-// against 216).  Above 128 rows an expert the larger tile reads the weights
-// less often (64 rows: 259 us against 309 for 256 x 256; with skewed routing and
-// 1536 x 2048, 128 rows 119 against 135, 256 rows 173 against 176, 512 rows 284
-// against 277).
+// against 215).  From some 96 rows an expert on the larger tile, which reads the
+// weights less often, is ahead (there 64 rows: 260 us against 264 for 256 x 256,
+// 128 rows 363 against 310; skewed routing and 1536 x 2048: 128 rows 118 against
+// 128, 256 rows 167 both, 512 rows 277 against 271).
 hipError_t launch_fp8_moe_gemm(GemmParams p, hipStream_t st) {
   // (a launch has fewer than 2^32 threads)
   const bool fits = rows_grid<1, 2, true>(p) < (int64_t(1) << 32) / (8 * kWave);
   if (p.numel <= 6 * int64_t(p.E) && fits) return rows_of<1, 2, 8, 1, true>(p, st);
-  if (p.numel <= 128 * int64_t(p.E)) return tile_launch<2, 4, 4, 4, 2, true>(p, st);
+  if (p.numel <= 96 * int64_t(p.E)) return tile_launch<2, 4, 4, 4, 2, true>(p, st);
   return tile_launch<2, 4, 8, 4, 2, true>(p, st);
 }
 

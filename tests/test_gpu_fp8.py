@@ -186,6 +186,25 @@ def test_gemm_nan_stays_in_its_row_and_column(M):
     fr.check_bf16(y[rows][:, cols], ref[rows][:, cols], fr.gemm_err(mag, 656)[rows][:, cols])
 
 
+@pytest.mark.parametrize("M,K,Ns", [(40, 272, 264), (3000, 272, 9000), (700, 144, 8200)])
+def test_gemm_infinite_and_nan_scales_stay_in_their_rows(M, K, Ns):
+    """Rows whose scale is infinite or NaN, also where a workgroup goes on to another tile."""
+    g = gen(M)
+    xq, xs = fr.whole_rows(g, M, K)
+    wq, ws = fr.whole_weights(g, 1, Ns, K)
+    bad = torch.arange(7, M, 31)
+    xs[:, bad[::2]] = float("inf")
+    xs[-1, bad[1::2]] = float("nan")
+    x, w, sc = _rows(xq, xs), wq.to(DEV), ws.to(DEV)
+    y = mla.moe_lora_fp8_gemm(x, w, sc)
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[bad] = False
+    keep = keep.to(DEV)
+    want = (_wide(x.q, x.scales)[keep] @ _wide_w(w, sc).view(Ns, K).t().contiguous()).to(BF)
+    assert torch.equal(y[keep], want)
+    assert not bool(torch.isfinite(y[~keep]).any())
+
+
 def test_gemm_leaves_what_is_behind_its_output():
     """The buffer goes on behind y: nothing is written there, at sizes that end inside a tile."""
     for M, Ns in ((5, 40), (70, 264), (300, 392)):
