@@ -444,7 +444,8 @@ MOE_LORA_API int moe_lora_accumulate(uint16_t *y, const uint16_t *delta, int64_t
  * moe_lora_rms_norm_fp8 -- for every row of x:
  *     h = bf16(x + residual)         (x itself when residual is NULL)
  *     v = h / sqrt(mean(h^2) + eps) * weight          (fp32)
- * h goes to residual_out, bf16(v) to y, v to q and scales.
+ * h goes to residual_out, bf16(v) to y, v to q and scales.  (A row whose sum of
+ * squares passes fp32's range has an infinite mean and comes out as zeros.)
  * [device] x, residual: bf16 [M, H] (residual may be NULL); weight: bf16 [H];
  *          residual_out: bf16 [M, H], NULL exactly when residual is; it may be
  *          residual or x itself; y: bf16 [M, H] or NULL (the rows the adapters
@@ -481,8 +482,8 @@ MOE_LORA_API int moe_lora_silu_mul_fp8(const uint16_t *y, int64_t P, int32_t I, 
  *          [S, ceil(Ns / 128), ceil(K / 128)]; y: bf16 [M, S*Ns], overlapping
  *          no input.
  * K a multiple of 16, Ns of 8; x, w and y 16-byte aligned.
- * MOE_LORA_ERR_UNSUPPORTED when a slice of w has 2^31 elements or more, S*Ns
- * does, or x_scales exceeds 2 GiB.  M == 0 does nothing.  Deterministic.
+ * MOE_LORA_ERR_UNSUPPORTED for K > 2^22, when a slice of w has 2^31 elements or
+ * more, S*Ns does, or x_scales exceeds 2 GiB.  M == 0 does nothing.  Deterministic.
  */
 MOE_LORA_API int moe_lora_fp8_gemm(const uint8_t *x, const float *x_scales, const uint8_t *w,
                    const float *w_scales, int64_t M, int32_t K, int32_t Ns, int32_t S,
@@ -504,7 +505,8 @@ MOE_LORA_API int moe_lora_fp8_gemm(const uint8_t *x, const float *x_scales, cons
  *          E, block_m; topk_weights: fp32 [M, topk], may be NULL when
  *          mul_routed_weight == 0; y: bf16 [M, topk, S*Ns], overlapping no
  *          input.
- * Sizes and alignment as moe_lora_align and moe_lora_fp8_gemm;
+ * Sizes and alignment as moe_lora_align and moe_lora_fp8_gemm; block_m is the
+ * align outputs' and sets no tile (blocks of one expert are taken together);
  * MOE_LORA_ERR_UNSUPPORTED also when x exceeds 2 GiB.  M == 0 does nothing.
  * Deterministic.
  */

@@ -75,7 +75,9 @@ __device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
 }
 
 // One workgroup of T threads a row; thread t holds the 8-column chunks t,
-// t + T, ... (CH of them).
+// t + T, ... (CH of them).  16384 x 4096 with the residual (9 bytes a value): 101
+// us, 6.0 TB/s, where a copy runs at 5.1; 16 x 2880 in a graph 2.5 us, of which
+// an empty kernel is 1.8.
 template <int T, int CH, bool RES>
 __global__ void __launch_bounds__(T) rms_norm_fp8_kernel(NormParams p) {
   __shared__ float part[T / kWave];
@@ -137,7 +139,8 @@ __global__ void __launch_bounds__(T) rms_norm_fp8_kernel(NormParams p) {
 }
 
 // 16 lanes a (row, block of 128 columns); a workgroup takes the same block of 16
-// consecutive rows, whose scales are neighbours.
+// consecutive rows, whose scales are neighbours.  65536 x 768 (7 bytes a value): 62
+// us, 5.7 TB/s; 64 workgroups a CU, 16 of them took 66 us.
 constexpr int kTS = 256, kRows = kTS / 16;
 __global__ void __launch_bounds__(kTS) silu_mul_fp8_kernel(SiluParams p, int32_t nb, int64_t items) {
   const int sub = threadIdx.x & 15;
