@@ -216,9 +216,11 @@ __device__ __forceinline__ void ring_barrier(int young) {
 
 // Work item -> (tile of rows, tile of columns).  Workgroups go to the XCDs in
 // turn, so each XCD takes one contiguous run of items, its workgroups in turn;
-// its L2 then holds that run's operands.  Within the run kGroup tiles of rows
-// share each column tile before the next one.
-constexpr int kGroup = 4;
+// its L2 then holds that run's operands.  Within the run G tiles of rows share
+// each column tile before the next one: 4 for dense rows (4096 x 4096 x 12288:
+// 182 us, alone 192, 16 of them 187), 1 for grouped ones, whose tiles seldom
+// have the same weights (120b-like w2, 32768 pairs: 458 us, 4 of them 489).
+template <int G>
 struct Items {
   uint32_t rows, cols;  // tiles of rows, tiles of columns (of all slices)
   uint32_t first, end;  // this XCD's run
@@ -232,8 +234,8 @@ struct Items {
     step = (gridDim.x - xcd + kXcds - 1) / kXcds;
   }
   __device__ __forceinline__ void at(uint32_t t, uint32_t* row, uint32_t* col) const {
-    const uint32_t grp = t / (kGroup * cols), base = grp * kGroup;
-    const uint32_t size = min(uint32_t(kGroup), rows - base), in = t - base * cols;
+    const uint32_t grp = t / (G * cols), base = grp * G;
+    const uint32_t size = min(uint32_t(G), rows - base), in = t - base * cols;
     *row = base + in % size;
     *col = in / size;
   }
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   } else {
     row_tiles = uint32_t((p.M + BM - 1) / BM);
   }
-  const Items items(row_tiles, uint32_t(p.S) * ntiles);
+  const Items<GROUPED ? 1 : 4> items(row_tiles, uint32_t(p.S) * ntiles);
   const int lane = lane_id(), w = wave_id(), wm = w / WN, wn = w % WN;
   const int a = lane & 15, g = lane >> 4;
   const int rl = lane >> 3, cl = lane & 7;  // row within a load, chunk as stored
