@@ -712,12 +712,14 @@ hipError_t rows_of(const GemmParams& p, hipStream_t st) {
 // 128 x 256 98; 256 x 256 175.
 hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
   const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
-  // Few rows: 16 columns a workgroup while that is not much over one a CU
-  // (4096 columns, K = 4096: 16 rows 6.2 us against 11.1 for the 64 x 64
-  // tile, 64 rows 13.2 against 11.1; 12288 columns, 16 rows: 13.3 against 11.1).
+  // Few rows: 16 columns a workgroup while those are not many over the CUs (K =
+  // 4096, against the 64 x 64 tile: 4096 columns, 16 rows 6.2 us and 11.1, 64 rows
+  // 13.2 and 11.1; 7568 columns, K = 2352, 16 rows 5.8 and 7.7; 7840 columns, K =
+  // 432, 28 rows 3.2 and 3.9; 12288 columns, 16 rows 13.3 and 11.1).
   const int64_t groups = int64_t(p.S) * ((p.Ns + 15) / 16);
-  if (p.M <= 16 && groups * 2 <= cus * 3) return rows_of<1, 1, 8, 2, false>(p, st);
-  if (p.M <= 64 && groups * ((p.M + 31) / 32) * 2 <= cus * 3) return rows_of<2, 1, 8, 1, false>(p, st);
+  if (p.M <= 16 && groups * 2 <= cus * 5) return rows_of<1, 1, 8, 2, false>(p, st);
+  if (p.M <= 32 && groups <= cus * 2) return rows_of<2, 1, 8, 1, false>(p, st);
+  if (p.M <= 64 && groups * 4 <= cus * 3) return rows_of<2, 1, 8, 1, false>(p, st);
   auto rounds = [&](int bm, int bn, int64_t at_once) {
     const int64_t tiles = (p.M + bm - 1) / bm * p.S * ((p.Ns + bn - 1) / bn);
     return (tiles + at_once - 1) / at_once;
