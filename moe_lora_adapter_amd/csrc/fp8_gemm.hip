@@ -37,10 +37,9 @@ __device__ __forceinline__ i32x8_t join(const uint4& a, const uint4& b) {
   return i32x8_t{int(a.x), int(a.y), int(a.z), int(a.w), int(b.x), int(b.y), int(b.z), int(b.w)};
 }
 
-// The sum of two byte offsets, past every range when either is: both are below
-// 2 GiB or kOob, and 2 kOob wraps to 0, so the sum saturates instead.
-__device__ __forceinline__ uint32_t at(uint32_t row, uint32_t k) {
-  return row == kOob || k == kOob ? kOob : row + k;
+// One float; past the range it reads as zero.
+__device__ __forceinline__ float buf_ld4(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
+  return __uint_as_float(uint32_t(__builtin_amdgcn_raw_buffer_load_b32(r, int(voff), 0, 0)));
 }
 
 // Where a block's rows come from and go to.
@@ -63,22 +62,27 @@ __device__ __forceinline__ RowMap row_of(const GemmParams& p, int64_t first, int
 // ---------------------------------------------------------------- few rows
 // One workgroup computes 16 MT rows x 16 NT columns: its KW wavefronts take
 // the K blocks w, w + KW, ... straight from memory (together they read KW x 128
-// consecutive bytes of each row of W) and add their sums in LDS, in order.  U
-// blocks of a wavefront are loaded before the first is multiplied.  Bound by
-// the stream of W: 20b-like decode w13 (64 pairs, 464 MB) 76 us, 6.2 TB/s; 32
-// columns a workgroup read X half as often as 16 (90 us), 64 leave too few
-// workgroups (86); more blocks ahead cost workgroups a CU (U = 2 87 us, 4 91).
-template <int MT, int NT, int KW, int U, bool GROUPED>
-__global__ void __launch_bounds__(KW * kWave) fp8_gemm_rows_kernel(GemmParams p, int ntiles) {
+// consecutive bytes of each row of W) and add their sums in LDS, in order.
+// Bound by the stream of W: 20b-like decode w13 (64 pairs, 464 MB) 81 us, 5.7
+// TB/s, with a wavefront's loads of one block ahead of its products; two blocks
+// ahead 83 us.  Grouped, the workgroups of a block take its pieces of 16 rows in
+// steps of `step` rows.
+constexpr int KW = 8;
+template <int MT, int NT, bool GROUPED>
+__global__ void __launch_bounds__(KW * kWave) fp8_gemm_rows_kernel(GemmParams p, int ntiles, int step) {
   __shared__ f32x4_t red[KW][MT * NT][kWave];
   const int tile = blockIdx.x % (p.S * ntiles);
-  const int64_t first = int64_t(blockIdx.x / (p.S * ntiles)) * 16 * MT;
+  int64_t first = int64_t(blockIdx.x / (p.S * ntiles)) * 16 * MT, stop = 0;
   int64_t e = 0;
   if constexpr (GROUPED) {
+    const int q = blockIdx.x / (p.S * ntiles), block = q % p.blocks;
+    first = int64_t(block) * p.block_m + q / p.blocks * (16 * MT);
+    stop = int64_t(block + 1) * p.block_m;
     // a block's pairs come first, its padding last: pieces of padding end here
-    if (first >= p.ntpp[0] || uint32_t(p.sorted[first]) >= uint32_t(p.numel)) return;
-    e = p.eids[first / p.block_m];
-    if (e < 0 || e >= p.E) return;
+    // (what is behind the last block is read too, in one wait, and not used)
+    const int32_t used = p.ntpp[0], lead = p.sorted[first];
+    e = p.eids[block];
+    if (first >= used || uint32_t(lead) >= uint32_t(p.numel) || e < 0 || e >= p.E) return;
   }
   const int slice = tile / ntiles, n0 = (tile % ntiles) * 16 * NT;
   const int lane = lane_id(), w = wave_id(), a = lane & 15, g = lane >> 4;
@@ -86,81 +90,86 @@ __global__ void __launch_bounds__(KW * kWave) fp8_gemm_rows_kernel(GemmParams p,
   const uint8_t* wbase = p.w + (e * p.S + slice) * p.Ns * int64_t(p.K);
   const auto wr = make_rsrc(wbase, uint32_t(p.Ns) * uint32_t(p.K));
   const float* wscale = p.ws + ((e * p.S + slice) * p.NB + n0 / kScaleBlock) * p.KB;
+  // An offset is below 2 GiB or, for rows and columns that are not there, kOob;
+  // so is an offset along K.  One of the two takes the sum out of range, which
+  // reads as zero; both wrap to 0, and what is read there reaches no output.
   uint32_t woff[NT];
 #pragma unroll
   for (int f = 0; f < NT; ++f) {
     const int n = n0 + 16 * f + a;
     woff[f] = n < p.Ns ? uint32_t(n) * uint32_t(p.K) + 16 * g : kOob;
   }
-  // rows of X: dense tiles are addressed from their first row, grouped ones
-  // from row 0 (X is below 2 GiB there)
-  const int64_t x0 = GROUPED ? 0 : first;
-  const int64_t xrows = GROUPED ? p.rows : std::min<int64_t>(p.rows - first, 16 * MT);
-  const auto xr = make_rsrc(p.x + x0 * p.K, uint32_t(xrows * p.K));
-  uint32_t xoff[MT];
-  int64_t srow[MT];
+  for (bool more = true; more;) {
+    more = GROUPED && first + step < stop && uint32_t(p.sorted[first + step]) < uint32_t(p.numel);
+    // rows of X: dense tiles are addressed from their first row, grouped ones
+    // from row 0 (X is below 2 GiB there)
+    const int64_t x0 = GROUPED ? 0 : first;
+    const int64_t xrows = GROUPED ? p.rows : std::min<int64_t>(p.rows - first, 16 * MT);
+    const auto xr = make_rsrc(p.x + x0 * p.K, uint32_t(xrows * p.K));
+    const auto sr = make_rsrc(p.xs, uint32_t(p.rows * p.KB) * 4);
+    uint32_t xoff[MT], soff[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const RowMap r = row_of<GROUPED>(p, first, 16 * i + a);
-    xoff[i] = r.x_row >= 0 ? uint32_t((r.x_row - x0) * p.K) + 16 * g : kOob;
-    srow[i] = r.x_row;
-  }
+    for (int i = 0; i < MT; ++i) {
+      const RowMap r = row_of<GROUPED>(p, first, 16 * i + a);
+      xoff[i] = r.x_row >= 0 ? uint32_t((r.x_row - x0) * p.K) + 16 * g : kOob;
+      soff[i] = r.x_row >= 0 ? uint32_t(r.x_row) * 4 : kOob;
+    }
 
-  f32x4_t acc[MT][NT];
+    f32x4_t acc[MT][NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int f = 0; f < NT; ++f) acc[i][f] = f32x4_t{0, 0, 0, 0};
+      for (int f = 0; f < NT; ++f) acc[i][f] = f32x4_t{0, 0, 0, 0};
 
-  for (int kb0 = w; kb0 < p.KB; kb0 += KW * U) {
-    i32x8_t wf[U][NT], xf[U][MT];
-    float sx[U][MT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = kb0 + u * KW;
+    for (int kb = w; kb < p.KB; kb += KW) {
       const uint32_t k = uint32_t(kb) * kScaleBlock;
-      const bool in = kb < p.KB;  // past the end everything reads as zero
-      const uint32_t lo = in && k + 16 * g < uint32_t(p.K) ? k : kOob;
-      const uint32_t hi = in && k + 64 + 16 * g < uint32_t(p.K) ? k + 64 : kOob;
-      const float sw = in ? wscale[kb] : 0.0f;
+      const uint32_t lo = k + 16 * g < uint32_t(p.K) ? k : kOob;
+      const uint32_t hi = k + 64 + 16 * g < uint32_t(p.K) ? k + 64 : kOob;
+      const float sw = wscale[kb];
+      i32x8_t wf[NT], xf[MT];
+      float sx[MT];
 #pragma unroll
       for (int f = 0; f < NT; ++f)
-        wf[u][f] = join(buf_ld16(wr, at(woff[f], lo), 0), buf_ld16(wr, at(woff[f], hi), 0));
+        wf[f] = join(buf_ld16(wr, woff[f] + lo, 0), buf_ld16(wr, woff[f] + hi, 0));
+      // the columns' loads first, a line's two halves together (in any order: 128
+      // experts of 2880 x 2880, 8 rows each, 213 us; so 196)
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        xf[u][i] = join(buf_ld16(xr, at(xoff[i], lo), 0), buf_ld16(xr, at(xoff[i], hi), 0));
-        sx[u][i] = in && srow[i] >= 0 ? p.xs[int64_t(kb) * p.rows + srow[i]] * sw : 0.0f;
+        sx[i] = buf_ld4(sr, soff[i] + uint32_t(kb) * uint32_t(p.rows) * 4);
+        xf[i] = join(buf_ld16(xr, xoff[i] + lo, 0), buf_ld16(xr, xoff[i] + hi, 0));
       }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int f = 0; f < NT; ++f) {
-          const f32x4_t d = mfma_e4m3(wf[u][f], xf[u][i]);
+          const f32x4_t d = mfma_e4m3(wf[f], xf[i]);
+          const float sc = sx[i] * sw;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][f][j] = fmaf(d[j], sx[u][i], acc[i][f][j]);
+          for (int j = 0; j < 4; ++j) acc[i][f][j] = fmaf(d[j], sc, acc[i][f][j]);
         }
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int f = 0; f < NT; ++f) red[w][i * NT + f][lane] = acc[i][f];
-  __syncthreads();
-  for (int t = w; t < MT * NT; t += KW) {
-    const int i = t / NT, f = t % NT;
-    f32x4_t s = red[0][t][lane];
-#pragma unroll
-    for (int v = 1; v < KW; ++v) s += red[v][t][lane];
-    const RowMap r = row_of<GROUPED>(p, first, 16 * i + a);
-    const int n = n0 + 16 * f + 4 * g;
-    if (r.y_row < 0 || n >= p.Ns) continue;
-    if constexpr (GROUPED) {
-      if (p.wt) s *= p.wt[r.y_row];
     }
-    uint2 o = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
-    *reinterpret_cast<uint2*>(p.y + r.y_row * (int64_t(p.S) * p.Ns) + slice * p.Ns + n) = o;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int f = 0; f < NT; ++f) red[w][i * NT + f][lane] = acc[i][f];
+    __syncthreads();
+    for (int t = w; t < MT * NT; t += KW) {
+      const int i = t / NT, f = t % NT;
+      f32x4_t s = red[0][t][lane];
+#pragma unroll
+      for (int v = 1; v < KW; ++v) s += red[v][t][lane];
+      const RowMap r = row_of<GROUPED>(p, first, 16 * i + a);
+      const int n = n0 + 16 * f + 4 * g;
+      if (r.y_row < 0 || n >= p.Ns) continue;
+      if constexpr (GROUPED) {
+        if (p.wt) s *= p.wt[r.y_row];
+      }
+      uint2 o = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+      *reinterpret_cast<uint2*>(p.y + r.y_row * (int64_t(p.S) * p.Ns) + slice * p.Ns + n) = o;
+    }
+    first += step;
+    if (more) __syncthreads();  // the sums have been read
   }
 }
 
@@ -689,18 +698,28 @@ hipError_t tile_launch(GemmParams p, hipStream_t st) {
   return hipSuccess;
 }
 
+// Pieces of an align block that start at once: as many as an expert has on
+// average, a block's workgroups take the others in turn.  Starting every piece
+// would leave most workgroups to find padding: 64 experts of 256 x 512, 8 rows
+// each in blocks of 64, 4.1 us and 8.5.
+template <int MT>
+int64_t parts_of(const GemmParams& p) {
+  const int64_t each = p.numel / (int64_t(p.E) * 12) + 1;
+  return std::min<int64_t>(each, p.block_m / (16 * MT));
+}
+
 template <int MT, int NT, bool GROUPED>
 int64_t rows_grid(const GemmParams& p) {
-  const int64_t pieces = GROUPED ? int64_t(p.blocks) * p.block_m / (16 * MT) : (p.M + 16 * MT - 1) / (16 * MT);
+  const int64_t pieces = GROUPED ? p.blocks * parts_of<MT>(p) : (p.M + 16 * MT - 1) / (16 * MT);
   return pieces * p.S * ((p.Ns + 16 * NT - 1) / (16 * NT));
 }
 
-template <int MT, int NT, int KW, int U, bool GROUPED>
+template <int MT, int NT, bool GROUPED>
 hipError_t rows_of(const GemmParams& p, hipStream_t st) {
   const int ntiles = (p.Ns + 16 * NT - 1) / (16 * NT);
   const int64_t grid = rows_grid<MT, NT, GROUPED>(p);
-  hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, NT, KW, U, GROUPED>), dim3(unsigned(grid)),
-                     dim3(KW * kWave), 0, st, p, ntiles);
+  hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, NT, GROUPED>), dim3(unsigned(grid)),
+                     dim3(KW * kWave), 0, st, p, ntiles, GROUPED ? int(parts_of<MT>(p)) * 16 * MT : 0);
   return hipGetLastError();
 }
 
@@ -712,20 +731,30 @@ hipError_t rows_of(const GemmParams& p, hipStream_t st) {
 // 128 x 256 98; 256 x 256 175.
 hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
   const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
-  // Few rows: 16 columns a workgroup while those are not many over the CUs (K =
-  // 4096, against the 64 x 64 tile: 4096 columns, 16 rows 6.2 us and 11.1, 64 rows
-  // 13.2 and 11.1; 7568 columns, K = 2352, 16 rows 5.8 and 7.7; 7840 columns, K =
-  // 432, 28 rows 3.2 and 3.9; 12288 columns, 16 rows 13.3 and 11.1).
-  const int64_t groups = int64_t(p.S) * ((p.Ns + 15) / 16);
-  if (p.M <= 16 && groups * 2 <= cus * 5) return rows_of<1, 1, 8, 2, false>(p, st);
-  if (p.M <= 32 && groups <= cus * 2) return rows_of<2, 1, 8, 1, false>(p, st);
-  if (p.M <= 64 && groups * 4 <= cus * 3) return rows_of<2, 1, 8, 1, false>(p, st);
   auto rounds = [&](int bm, int bn, int64_t at_once) {
     const int64_t tiles = (p.M + bm - 1) / bm * p.S * ((p.Ns + bn - 1) / bn);
     return (tiles + at_once - 1) / at_once;
   };
-  const int64_t r0 = rounds(64, 64, cus);
-  const int64_t cost[5] = {r0 == 1 ? 36 : 50 * rounds(64, 64, 2 * cus), 43 * rounds(64, 128, cus),
+  const int64_t r0 = rounds(64, 64, cus), r0x2 = rounds(64, 64, 2 * cus);
+  // Few rows, straight from memory: estimates in microseconds for them, which read
+  // all of W for every 32 rows, or take 1.6 ns a workgroup, and for the 64 x 64 tile,
+  // whose time is the latency of K.  Measured, the two: 16 rows of 4096 x 4096 6.1 and 10.4, of 4096 x 9600
+  // 13.7 and 10.5, of 1024 x 9600 4.9 and 4.8; 32 rows of 4096 x 4096 8.0 and 10.6,
+  // of 4096 x 7840 13.3 and 10.5; 64 rows of 4096 x 2880 13.3 and 11.6; 72 of 3488 x
+  // 528 5.3 and 10.2; 482 of 32 x 3512 7.5 and 4.5.
+  const int64_t groups = int64_t(p.S) * ((p.Ns + 15) / 16), passes = (p.M + 31) / 32;
+  const double mb = 1e-6 * p.S * p.Ns * p.K;
+  const double by_rows = 1.8 + 5e-4 * p.K + std::max(mb * (p.M <= 16 ? 0.18 : 0.3 * double(passes)),
+                                                     (p.M <= 16 ? 8e-4 : 1.6e-3) * double(groups * passes));
+  const double by_tile = 2.9 + 1.9e-3 * p.K * (r0 == 1 ? 1.0 : 1.4 * double(r0x2));
+  // (1024 rows: their scales stay below 2 GiB)
+  if (by_rows < by_tile && p.M <= 1024) {
+    // (16 rows: up to a CU's worth of groups of 16 columns 6.1 us, in 32s 7.8, 4096
+    // x 4096; beyond, 2880 x 5120, 6.0 and 4.9)
+    if (p.M > 16) return rows_of<2, 1, false>(p, st);
+    return groups <= cus ? rows_of<1, 1, false>(p, st) : rows_of<1, 2, false>(p, st);
+  }
+  const int64_t cost[5] = {r0 == 1 ? 36 : 50 * r0x2, 43 * rounds(64, 128, cus),
                            63 * rounds(128, 128, cus), 98 * rounds(128, 256, cus),
                            175 * rounds(256, 256, cus)};
   switch (std::min_element(cost, cost + 5) - cost) {
@@ -737,18 +766,44 @@ hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
   }
 }
 
-// Up to six rows an expert the weights' stream is all there is, and 32 columns
-// a workgroup, straight from memory, run it fastest (128 experts of 2880 x
-// 2880: 4 rows each 189 us against 209 for the 128 x 256 tile, 8 rows 224
-// against 215).  From some 96 rows an expert on the larger tile, which reads the
-// weights less often, is ahead (there 64 rows: 260 us against 264 for 256 x 256,
-// 128 rows 363 against 310; skewed routing and 1536 x 2048: 128 rows 118 against
-// 128, 256 rows 167 both, 512 rows 277 against 271).
+// Estimates in microseconds, with the pairs spread evenly: `stream`, one expert's
+// weights at 5.5 TB/s.  The rows kernel takes 3 us, and for each piece of 16 rows
+// those weights or 4 ns a workgroup; the tiles take 10 us, of which most is
+// finding them, and each expert's weights once, or, with few of them, the
+// latency of their K.  Measured, rows and tiles: 8 experts of 512 x 1024, 8 rows
+// each, 3.4 and 9.3, 96 rows 8.5 and 10.7; 8 of 2048 x 4096, 8 rows 14.5 and
+// 23.6, 48 rows 39 and 27; 128 of 2880 x 2880, 4 rows 181 and 192, 8 rows 199 and
+// 200, 16 rows 254 and 209.
 hipError_t launch_fp8_moe_gemm(GemmParams p, hipStream_t st) {
+  const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
+  const int64_t E = p.E, used = std::min<int64_t>(p.numel, E);
+  // tiles of `rows` rows
+  auto tiles = [&](int rows) { return std::min<int64_t>(p.numel, std::max(used, p.numel / rows + E / 2)); };
+  const double stream = double(p.S) * p.Ns * p.K / 5.5e6;
+  const double groups = double(p.S) * ((p.Ns + 31) / 32);
+  const double by_rows = 3 + double(tiles(16)) * std::max(stream, 0.004 * groups);
+  const double by_tiles = 10 + std::max(0.45 * p.KB, 0.2 * p.KB + double(used) * stream);
   // (a launch has fewer than 2^32 threads)
   const bool fits = rows_grid<1, 2, true>(p) < (int64_t(1) << 32) / (8 * kWave);
-  if (p.numel <= 6 * int64_t(p.E) && fits) return rows_of<1, 2, 8, 1, true>(p, st);
-  if (p.numel <= 96 * int64_t(p.E)) return tile_launch<2, 4, 4, 4, 2, true>(p, st);
+  if (by_rows <= by_tiles && fits) {
+    // 64 columns a workgroup read X half as often as 32, which is worth it from a
+    // few rows an expert on and with a workgroup for every CU (64 experts of 1024
+    // x 4096: 1 row each 36.3 us and 32.7, 8 rows 52.3 and 53.7; 128 of 2880 x
+    // 2880, 8 rows 199 and 215; 8 of 512 x 1024, 8 rows 4.0 and 3.4)
+    if (p.numel >= 3 * E && used * p.S * ((p.Ns + 63) / 64) >= cus) return rows_of<1, 4, true>(p, st);
+    return rows_of<1, 2, true>(p, st);
+  }
+  // The tile whose rounds over the device cost least, the largest only with enough
+  // rows to fill it whatever the routing.  (64 x 256, 128 x 256 and 256 x 256) 128
+  // experts of 1536 x 2048: 32 rows each 82, 83 and 87 us, 64 rows 106, 91 and
+  // 95, 128 rows 132, 122 and 112; of 2880 x 2880, 128 rows 408, 319 and 298; 16 of
+  // 2048 x 4096: 96 rows 45, 50 and 52, 192 rows 68, 51 and 63, 256 rows 87, 82
+  // and 68; skewed routing over 64 of 1024 x 1024, 96 rows: 30, 30 and 39.
+  const int64_t cols = p.S * ((p.Ns + 255) / 256);
+  auto rounds = [&](int rows) { return (tiles(rows) * cols + cus - 1) / cus; };
+  const int64_t cost64 = 80 * rounds(64), cost128 = 98 * rounds(128), cost256 = 140 * rounds(256);
+  if (p.block_m <= 64 && cost64 <= cost128) return tile_launch<2, 4, 2, 4, 3, true>(p, st);
+  if (p.numel <= 96 * E || cost128 <= cost256) return tile_launch<2, 4, 4, 4, 2, true>(p, st);
   return tile_launch<2, 4, 8, 4, 2, true>(p, st);
 }
 

@@ -506,3 +506,50 @@ def test_stream_argument():
     mla.moe_lora_fp8_gemm(x, w, sc, y, stream=s)
     s.synchronize()
     assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
+# Enough weights for each of the tiles, and the 64-column rows kernel, at odd sizes: the same list's
+# columns as MOE.
+MOE_WIDE = [
+    (1040, 1, 2192, 1032, 1, 4, 64, False, True, "invalid"),
+    (400, 4, 2064, 520, 1, 4, 16, True, False, "uniform"),
+    (700, 2, 1168, 520, 2, 7, 32, False, True, "twice"),
+    (60, 8, 400, 1288, 2, 20, 32, False, False, "uniform"),
+    (700, 2, 1168, 520, 2, 7, 128, True, True, "invalid"),
+    (600, 2, 1040, 776, 2, 4, 128, False, False, "twice"),
+    (1000, 4, 784, 1544, 1, 3, 32, False, True, "invalid"),
+    (1000, 2, 656, 1032, 2, 3, 128, True, True, "uniform"),
+    (800, 2, 656, 1032, 2, 4, 64, False, True, "one"),
+    (70, 2, 784, 456, 2, 16, 64, False, True, "invalid"),
+    (300, 4, 528, 776, 1, 48, 16, True, False, "uniform"),
+    (90, 2, 272, 2056, 1, 8, 128, False, True, "one"),
+    (250, 2, 144, 1080, 1, 16, 64, False, True, "invalid"),
+    (3, 2, 1328, 1304, 2, 64, 64, False, True, "uniform"),
+]
+
+
+@pytest.mark.parametrize("case", MOE_WIDE)
+def test_moe_gemm_wide(case):
+    test_moe_gemm(case)
+
+
+@pytest.mark.parametrize("case", MOE_WIDE)
+def test_moe_gemm_wide_whole_numbers_exactly(case):
+    test_moe_gemm_whole_numbers_exactly(case)
+
+
+@pytest.mark.parametrize("M,K,Ns,B", [(60, 272, 136, 16), (120, 400, 1288, 64), (800, 784, 1544, 32),
+                                      (800, 784, 1544, 128)])
+def test_moe_gemm_reads_no_meaning_behind_the_last_block(M, K, Ns, B):
+    """Whatever the align outputs hold behind num_tokens_post_padded, and experts out of range."""
+    case = (M, 2, K, Ns, 1, 4, B, True, True, "uniform")
+    ids, xq, xs, wq, ws, tw, y0 = _moe(*case)
+    al = _base_align(ids, 4, B)
+    n = int(al.num_tokens_post_padded.item())
+    al.sorted_token_ids.view(-1)[n:] = 0
+    al.expert_ids.view(-1)[n // B:] = 3
+    al.expert_ids[0, :n // B][al.expert_ids[0, :n // B] == 2] = -1
+    y = y0.to(DEV)
+    mla.moe_lora_fp8_moe_gemm(_rows(xq, xs), wq.to(DEV), ws.to(DEV), al, tw.to(DEV), y,
+                              mul_routed_weight=True, x_per_pair=True)
+    _check_moe(y, y0, ids, xq, xs, wq, ws, tw, True, True, skip=(2,))
