@@ -736,19 +736,20 @@ hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
     return (tiles + at_once - 1) / at_once;
   };
   const int64_t r0 = rounds(64, 64, cus), r0x2 = rounds(64, 64, 2 * cus);
-  // Few rows, straight from memory: estimates in microseconds for them, which read
-  // all of W for every 32 rows, or take 1.6 ns a workgroup, and for the 64 x 64 tile,
-  // whose time is the latency of K.  Measured, the two: 16 rows of 4096 x 4096 6.1 and 10.4, of 4096 x 9600
-  // 13.7 and 10.5, of 1024 x 9600 4.9 and 4.8; 32 rows of 4096 x 4096 8.0 and 10.6,
-  // of 4096 x 7840 13.3 and 10.5; 64 rows of 4096 x 2880 13.3 and 11.6; 72 of 3488 x
-  // 528 5.3 and 10.2; 482 of 32 x 3512 7.5 and 4.5.
+  // Few rows or columns, straight from memory: estimates in microseconds for that,
+  // which reads all of W for every 32 rows, or takes 1.6 ns a workgroup, and for the
+  // 64 x 64 tile, whose time is the latency of K.  Measured, the two: 16 rows of
+  // 4096 x 4096 6.1 and 10.4, of 4096 x 9600 13.7 and 10.5, of 1024 x 9600 4.9 and
+  // 4.8; 32 rows of 4096 x 4096 8.0 and 10.6, of 4096 x 7840 13.3 and 10.5; 64 rows
+  // of 4096 x 2880 13.3 and 11.6; 72 of 3488 x 528 5.3 and 10.2; 482 of 32 x 3512 7.5
+  // and 4.5; 1463 of 4016 x 32 6.3 and 10.5.
   const int64_t groups = int64_t(p.S) * ((p.Ns + 15) / 16), passes = (p.M + 31) / 32;
   const double mb = 1e-6 * p.S * p.Ns * p.K;
   const double by_rows = 1.8 + 5e-4 * p.K + std::max(mb * (p.M <= 16 ? 0.18 : 0.3 * double(passes)),
                                                      (p.M <= 16 ? 8e-4 : 1.6e-3) * double(groups * passes));
   const double by_tile = 2.9 + 1.9e-3 * p.K * (r0 == 1 ? 1.0 : 1.4 * double(r0x2));
-  // (1024 rows: their scales stay below 2 GiB)
-  if (by_rows < by_tile && p.M <= 1024) {
+  // (it addresses the scales of all rows within 2 GiB)
+  if (by_rows < by_tile && p.M * p.KB < int64_t(1) << 29) {
     // (16 rows: up to a CU's worth of groups of 16 columns 6.1 us, in 32s 7.8, 4096
     // x 4096; beyond, 2880 x 5120, 6.0 and 4.9)
     if (p.M > 16) return rows_of<2, 1, false>(p, st);
