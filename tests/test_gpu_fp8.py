@@ -553,3 +553,38 @@ def test_moe_gemm_reads_no_meaning_behind_the_last_block(M, K, Ns, B):
     mla.moe_lora_fp8_moe_gemm(_rows(xq, xs), wq.to(DEV), ws.to(DEV), al, tw.to(DEV), y,
                               mul_routed_weight=True, x_per_pair=True)
     _check_moe(y, y0, ids, xq, xs, wq, ws, tw, True, True, skip=(2,))
+
+
+# Enough columns for the tiles, and for 32 columns a workgroup, at odd sizes: the same list's columns
+# as GEMM.
+GEMM_WIDE = [(3, 272, 6040, 2), (16, 144, 5000, 1), (90, 656, 4104, 1), (70, 1168, 2056, 2),
+             (300, 1168, 2056, 1), (200, 2192, 4104, 1), (500, 784, 4104, 1), (520, 1296, 4104, 1),
+             (1000, 1040, 5128, 1), (777, 2064, 3592, 1)]
+
+
+@pytest.mark.parametrize("M,K,Ns,S", GEMM_WIDE)
+def test_gemm_wide(M, K, Ns, S):
+    test_gemm(M, K, Ns, S)
+
+
+@pytest.mark.parametrize("M,K,Ns,S", GEMM_WIDE)
+def test_gemm_wide_whole_numbers_exactly(M, K, Ns, S):
+    test_gemm_whole_numbers_exactly(M, K, Ns, S)
+
+
+@pytest.mark.parametrize("M,K,Ns", [(16, 144, 5000), (90, 656, 4104), (500, 784, 4104), (1000, 1040, 5128)])
+def test_gemm_wide_nan_stays_in_its_row_and_column(M, K, Ns):
+    xq, xs, wq, ws = _gemm(M, K, Ns, 1, M)
+    ref, mag = fr.gemm(xq, xs, wq, ws)
+    xq[M - 2, K - 6] = float("nan")
+    wq[0, Ns - 3, 3] = float("nan")
+    y = mla.moe_lora_fp8_gemm(_rows(xq, xs), wq.to(DEV), ws.to(DEV)).cpu()
+    assert torch.isnan(y[M - 2]).all() and torch.isnan(y[:, Ns - 3]).all()
+    rows, cols = torch.arange(M) != M - 2, torch.arange(Ns) != Ns - 3
+    fr.check_bf16(y[rows][:, cols], ref[rows][:, cols], fr.gemm_err(mag, K)[rows][:, cols])
+
+
+def test_gemm_many_rows_of_few_columns():
+    """Straight from memory at many rows: the scales' offsets, and K of many blocks."""
+    test_gemm_whole_numbers_exactly(5512, 352, 24, 1)
+    test_gemm_whole_numbers_exactly(1463, 4016, 40, 1)
