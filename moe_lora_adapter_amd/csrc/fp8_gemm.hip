@@ -16,6 +16,7 @@
 // below its exponent, and the eights in fp32; every sum outside it is fp32, and
 // Y is rounded to bf16 once.
 #include <algorithm>
+#include <cmath>
 
 #include "common.h"
 #include "dma.h"
@@ -353,35 +354,46 @@ struct TileList {
 // 1.97 GHz the load leaves.  Without the loads the same loop takes 141 us, the
 // loads alone 89: what is between is stages whose loads take longer than their
 // MFMAs, with two of them filling the LDS.
-template <int WM, int WN, int FM, int FN, int NS>
+//
+// KG > 1, for small tiles: a stage has KG blocks of 128, each of which WM x WN
+// wavefronts multiply, and their sums meet in LDS.  A CU takes in some 64 KB a
+// microsecond whatever its tile, so where there are few tiles they are small (64
+// x 4096 x 4096: 32 x 32 with KG = 4 9.5 us, 64 x 64 with one block a stage 13.2,
+// with two 13.8).
+template <int WM, int WN, int FM, int FN, int NS, int KG = 1>
 struct Tile {
-  static constexpr int BM = WM * FM * 16, BN = WN * FN * 16, NW = WM * WN;
-  static constexpr int XI = BM / 8 / NW, WI = BN / 8 / NW;  // 1 KiB loads a wavefront and stage
-  static constexpr int kLoads = XI + WI + 1;
-  static constexpr int kX = 0, kW = BM * 128, kS = kW + BN * 128, kStage = kS + BM * 4 + 256;
+  static constexpr int BM = WM * FM * 16, BN = WN * FN * 16, NW = WM * WN * KG;
+  static constexpr int XI = BM / 8 / NW, WI = BN / 8 / NW;  // 1 KiB loads a wavefront and K block
+  static constexpr int kEach = XI + WI + 1, kLoads = KG * kEach;
+  static constexpr int kSegs = (BM + kWave - 1) / kWave;  // loads of the rows' scales
+  static constexpr int kX = 0, kW = BM * 128, kS = kW + BN * 128, kBlock = kS + kSegs * 256 + 256;
+  static constexpr int kStage = KG * kBlock;
+  static constexpr int kJoin = NS * kStage;  // (KG > 1) sums of the other wavefronts
   // the rows' pairs and weights of the tile being stored, of those whose stages
   // are in the ring (one each where K is one block), and of the next to load
   static constexpr int kPairs = NS * kStage, kRing = NS + 2, kList = kPairs + kRing * BM * 8;
   static constexpr int lds_bytes(bool grouped) {
-    return grouped ? kList + int(sizeof(TileList)) : kPairs;
+    return grouped ? kList + int(sizeof(TileList)) : kPairs + (KG - 1) * BM * BN * 4;
   }
   // workgroups of a CU, by LDS and by two wavefronts a SIMD
   static constexpr int groups(bool grouped) {
     const int a = 160 * 1024 / lds_bytes(grouped), b = 8 / NW;
     return a < b ? a : b;
   }
-  static_assert(XI * 8 * NW == BM && WI * 8 * NW == BN && BM % kWave == 0, "tile");
-  static_assert(BM / kWave < NW && FM % 2 == 0 && FN % 2 == 0 && NS >= 2, "tile");
+  static_assert(XI * 8 * NW == BM && WI * 8 * NW == BN, "tile");
+  static_assert(kSegs < NW && FM % 2 == 0 && FN % 2 == 0 && NS >= 2, "tile");
 };
 
-template <int WM, int WN, int FM, int FN, int NS, bool GROUPED>
-__global__ void __launch_bounds__(WM * WN * kWave, 2)
+template <int WM, int WN, int FM, int FN, int NS, bool GROUPED, int KG>
+__global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
     fp8_gemm_tile_kernel(GemmParams p, int ntiles) {
-  using T = Tile<WM, WN, FM, FN, NS>;
+  using T = Tile<WM, WN, FM, FN, NS, KG>;
   constexpr int BM = T::BM, BN = T::BN, XI = T::XI, WI = T::WI, kLoads = T::kLoads;
   // whether the columns' loads run ahead of the rows' (below)
   constexpr bool kEarly = FM > 2;
+  static_assert(KG == 1 || (!GROUPED && !kEarly), "a stage of several K blocks");
   constexpr int kX = T::kX, kW = T::kW, kS = T::kS, kStage = T::kStage;
+  const int stages = (p.KB + KG - 1) / KG;  // of a tile
   __shared__ __align__(1024) uint8_t lds[T::lds_bytes(GROUPED)];
 
   TileList* list = reinterpret_cast<TileList*>(lds + T::kList);
@@ -396,7 +408,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     row_tiles = uint32_t((p.M + BM - 1) / BM);
   }
   const Items<GROUPED ? 1 : 4> items(row_tiles, uint32_t(p.S) * ntiles);
-  const int lane = lane_id(), w = wave_id(), wm = w / WN, wn = w % WN;
+  const int lane = lane_id(), w = wave_id(), kg = w / (WM * WN), wm = w / WN % WM, wn = w % WN;
   const int a = lane & 15, g = lane >> 4;
   const int rl = lane >> 3, cl = lane & 7;  // row within a load, chunk as stored
   auto swizzle = [](int r) { return (r & 3) | ((r >> 1) & 4); };  // bits 0, 1, 3
@@ -413,7 +425,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   // i.  The columns' chunk order has two forms, by bit 3 of the column.
   const int xc = 16 * (cl ^ rl), wc = 16 * (cl ^ swizzle(rl));
   uint32_t xoff, woff, woff1, soff;
-  constexpr int kSegs = BM / kWave, kCols = (BN + kScaleBlock - 1) / kScaleBlock;
+  constexpr int kSegs = T::kSegs, kCols = (BN + kScaleBlock - 1) / kScaleBlock;
   const int sdst = kS + 256 * std::min(w, kSegs);
   const uint32_t sstride = w < kSegs ? uint32_t(p.rows) * 4 : 4;
   const uint32_t step8 = 8 * uint32_t(p.K);
@@ -485,9 +497,11 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   // zeros; behind the last tile everything does, so that every stage counts the
   // same loads.
   auto load = [&](int l) {
-    const uint32_t st = base + uint32_t(lstage) * kStage;
-    const int have = p.K - lkb * kScaleBlock;
-    const uint32_t k = uint32_t(lkb) * kScaleBlock;
+    const int kb = KG == 1 ? lkb : lkb * KG + l / T::kEach;
+    const uint32_t st = base + uint32_t(lstage) * kStage + uint32_t(l / T::kEach * T::kBlock);
+    l %= T::kEach;
+    const int have = p.K - kb * kScaleBlock;
+    const uint32_t k = uint32_t(kb) * kScaleBlock;
     if (l < XI) {
       const uint32_t o = GROUPED ? __builtin_amdgcn_ds_bpermute(4 * (8 * l + rl), xoff) + xc
                                  : xoff + uint32_t(l) * step8;
@@ -498,7 +512,9 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
       tile_dma16(wr, st + kW + 1024 * (w * WI + i),
                  (wc ^ flip) < have ? (flip ? woff1 : woff) + uint32_t(i) * step8 : kOob, k);
     } else {
-      tile_dma4(sr, st + sdst, soff, uint32_t(lkb) * sstride);
+      // (a stage's second block may be past K: its scales are zeros, too)
+      const bool in = KG == 1 || kb < p.KB;
+      tile_dma4(sr, st + sdst, in ? soff : kOob, uint32_t(in ? kb : 0) * sstride);
     }
   };
   auto loaded = [&]() {  // a stage's loads are all issued
@@ -514,9 +530,10 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
 
   // ---- the multiplying side
   const int xrow = wm * FM * 16 + a, wrow = wn * FN * 16 + 8 * (a >> 2) + (a & 3);
-  const int xo = kX + xrow * 128 + 16 * (g ^ (a & 7));
-  const int wo = kW + wrow * 128 + 16 * (g ^ (a & 7));
-  const int so = kS + BM * 4 + wn * FN * 16 / kScaleBlock * 4;  // this wavefront's column block
+  const int ko = kg * T::kBlock;  // this wavefront's K block of a stage
+  const int xo = ko + kX + xrow * 128 + 16 * (g ^ (a & 7));
+  const int wo = ko + kW + wrow * 128 + 16 * (g ^ (a & 7));
+  const int so = ko + kS + kSegs * 256 + wn * FN * 16 / kScaleBlock * 4;  // this wavefront's column block
   constexpr int kWait = (NS - 2) * kLoads + (kEarly ? WI : 0);  // younger loads at a stage's barrier
 
   set_tile();
@@ -525,7 +542,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
 #pragma unroll
     for (int l = 0; l < kLoads; ++l) load(l);
     loaded();
-    if (lkb == p.KB) next_loads();
+    if (lkb == stages) next_loads();
   }
   stage_barrier<(NS - 1) * kLoads>();
   int stage = 0, ring = 0;
@@ -543,7 +560,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
       none |= int64_t(row) * BM + wm * FM * 16 >= p.M;
     }
     if (none) {
-      for (int kb = 0; kb < p.KB; ++kb) {
+      for (int kb = 0; kb < stages; ++kb) {
         if constexpr (kEarly) {
           asm volatile("s_barrier" ::: "memory");
 #pragma unroll
@@ -555,8 +572,9 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
           if (!kEarly || l < XI || l == kLoads - 1) load(l);
         loaded();
         stage = stage + 1 == NS ? 0 : stage + 1;
-        if (lkb == p.KB) next_loads();
+        if (lkb == stages) next_loads();
       }
+      if constexpr (KG > 1) asm volatile("s_barrier" ::: "memory");  // of the sums
       young = 0;
       continue;
     }
@@ -586,7 +604,7 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     auto rows = [&](const uint8_t* st, int i) {
       xf[i & 1] = join(*reinterpret_cast<const uint4*>(st + xo + 2048 * i),
                        *reinterpret_cast<const uint4*>(st + (xo ^ 64) + 2048 * i));
-      sx[i & 1] = *reinterpret_cast<const float*>(st + kS + 4 * (xrow + 16 * i));
+      sx[i & 1] = *reinterpret_cast<const float*>(st + ko + kS + 4 * (xrow + 16 * i));
     };
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
@@ -597,9 +615,9 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
     }
     rows(lds + stage * kStage, 0);
     sw = *reinterpret_cast<const float*>(lds + stage * kStage + so);
-    for (int kb = 0; kb < p.KB;) {
+    for (int kb = 0; kb < stages;) {
       // the stages until the loads change their tile
-      const int n = std::min(p.KB - kb, p.KB - lkb);
+      const int n = std::min(stages - kb, stages - lkb);
       for (int r = 0; r < n; ++r) {
         const uint8_t* st = lds + stage * kStage;
         stage = stage + 1 == NS ? 0 : stage + 1;
@@ -643,11 +661,27 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
         loaded();
       }
       kb += n;
-      if (lkb == p.KB) next_loads();
+      if (lkb == stages) next_loads();
     }
 #pragma unroll
     for (int f = 0; f < FN; ++f) add(FM - 1, f);
 
+    if constexpr (KG > 1) {
+      // The first wavefronts add the others' sums, in order, and store.  The next
+      // sums are written behind a stage's barrier, when these have been read.
+      f32x4_t* other = reinterpret_cast<f32x4_t*>(lds + T::kJoin) + (w % (WM * WN)) * FM * FN * kWave + lane;
+      constexpr int kAll = WM * WN * FM * FN * kWave;
+      if (kg > 0) {
+#pragma unroll
+        for (int j = 0; j < FM * FN; ++j) other[(kg - 1) * kAll + j * kWave] = acc[j / FN][j % FN];
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (kg > 0) continue;
+#pragma unroll
+      for (int j = 0; j < FM * FN; ++j)
+#pragma unroll
+        for (int v = 0; v < KG - 1; ++v) acc[j / FN][j % FN] += other[v * kAll + j * kWave];
+    }
     const int nl = n0 + wn * FN * 16 + 8 * g;  // this lane's columns: 8 of each 32
     int stores = 0;  // of this wavefront
 #pragma unroll
@@ -680,9 +714,9 @@ __global__ void __launch_bounds__(WM * WN * kWave, 2)
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 }
 
-template <int WM, int WN, int FM, int FN, int NS, bool GROUPED>
+template <int WM, int WN, int FM, int FN, int NS, bool GROUPED, int KG = 1>
 hipError_t tile_launch(GemmParams p, hipStream_t st) {
-  using T = Tile<WM, WN, FM, FN, NS>;
+  using T = Tile<WM, WN, FM, FN, NS, KG>;
   const int ntiles = (p.Ns + T::BN - 1) / T::BN;
   const int64_t resident = int64_t(std::max(xcd_compute_units(), 1)) * kXcds * T::groups(GROUPED);
   const int32_t all = GROUPED ? p.blocks : int32_t((p.M + T::BM - 1) / T::BM);
@@ -690,7 +724,7 @@ hipError_t tile_launch(GemmParams p, hipStream_t st) {
   for (p.block0 = 0; p.block0 < all; p.block0 += most) {
     p.blocks = std::min(most, all - p.block0);
     const int64_t grid = std::min(int64_t(p.blocks) * p.S * ntiles, resident);
-    hipLaunchKernelGGL((fp8_gemm_tile_kernel<WM, WN, FM, FN, NS, GROUPED>), dim3(unsigned(grid)),
+    hipLaunchKernelGGL((fp8_gemm_tile_kernel<WM, WN, FM, FN, NS, GROUPED, KG>), dim3(unsigned(grid)),
                        dim3(T::NW * kWave), 0, st, p, ntiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -725,40 +759,44 @@ hipError_t rows_of(const GemmParams& p, hipStream_t st) {
 
 }  // namespace
 
-// The tile whose rounds over the device cost least.  A round's time for each
-// 128 of K, in hundredths of a microsecond (measured at K = 4096 with every
-// CU busy): 64 x 64 36, or 50 with two on a CU; 64 x 128 43; 128 x 128 63;
-// 128 x 256 98; 256 x 256 175.
+// Estimates in microseconds.  The tiles above 32 x 32: 3 us, and for each 128 of K
+// the hundredths that a round over the device takes (measured at K = 4096 with
+// every CU busy: 64 x 64 30, or 50 with two on a CU; 64 x 128 43; 128 x 128 63; 128 x
+// 256 98; 256 x 256 175).  The 32 x 32 tile, where there is a CU for each.  Few rows
+// or columns straight from memory: all of W for every 32 rows, or 1.6 ns a
+// workgroup.
+//
+// Measured, with W from memory, not from the cache in front of it, straight, 32 x
+// 32 and 64 x 64: 16 rows of 4096 x 4096 6.9, 8.9 and 11.6 us, of 8192 x 8192 16.5,
+// 15.4 and 21.5; 32 rows of 4096 x 4096 8.8, 9.4 and 11.8, of 4096 x 7840 14.5, 10.6
+// and 12.8; 64 rows of 4096 x 4096 14.3, 9.5 and 13.2, of 4096 x 12288 36, 22 and
+// 16; 100 of 8192 x 2048 24.6, 13.5 and 22.1; 482 of 32 x 3512 7.5, - and 4.5; 1463
+// of 4016 x 32 6.3, - and 10.5.
 hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
   const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
   auto rounds = [&](int bm, int bn, int64_t at_once) {
     const int64_t tiles = (p.M + bm - 1) / bm * p.S * ((p.Ns + bn - 1) / bn);
     return (tiles + at_once - 1) / at_once;
   };
-  const int64_t r0 = rounds(64, 64, cus), r0x2 = rounds(64, 64, 2 * cus);
-  // Few rows or columns, straight from memory: estimates in microseconds for that,
-  // which reads all of W for every 32 rows, or takes 1.6 ns a workgroup, and for the
-  // 64 x 64 tile, whose time is the latency of K.  Measured, the two: 16 rows of
-  // 4096 x 4096 6.1 and 10.4, of 4096 x 9600 13.7 and 10.5, of 1024 x 9600 4.9 and
-  // 4.8; 32 rows of 4096 x 4096 8.0 and 10.6, of 4096 x 7840 13.3 and 10.5; 64 rows
-  // of 4096 x 2880 13.3 and 11.6; 72 of 3488 x 528 5.3 and 10.2; 482 of 32 x 3512 7.5
-  // and 4.5; 1463 of 4016 x 32 6.3 and 10.5.
+  const bool once32 = rounds(32, 32, cus) == 1, once64 = rounds(64, 64, cus) == 1;
+  const int64_t cost[5] = {once64 ? 30 : 50 * rounds(64, 64, 2 * cus), 43 * rounds(64, 128, cus),
+                           63 * rounds(128, 128, cus), 98 * rounds(128, 256, cus),
+                           175 * rounds(256, 256, cus)};
+  const int best = int(std::min_element(cost, cost + 5) - cost);
   const int64_t groups = int64_t(p.S) * ((p.Ns + 15) / 16), passes = (p.M + 31) / 32;
   const double mb = 1e-6 * p.S * p.Ns * p.K;
   const double by_rows = 1.8 + 5e-4 * p.K + std::max(mb * (p.M <= 16 ? 0.18 : 0.3 * double(passes)),
                                                      (p.M <= 16 ? 8e-4 : 1.6e-3) * double(groups * passes));
-  const double by_tile = 2.9 + 1.9e-3 * p.K * (r0 == 1 ? 1.0 : 1.4 * double(r0x2));
-  // (it addresses the scales of all rows within 2 GiB)
-  if (by_rows < by_tile && p.M * p.KB < int64_t(1) << 29) {
+  const double by_32 = once32 ? 3.5 + 1.4e-3 * p.K : INFINITY;
+  const double by_tile = 3 + 0.01 * p.KB * double(cost[best]);
+  if (by_rows < std::min(by_32, by_tile)) {
     // (16 rows: up to a CU's worth of groups of 16 columns 6.1 us, in 32s 7.8, 4096
     // x 4096; beyond, 2880 x 5120, 6.0 and 4.9)
     if (p.M > 16) return rows_of<2, 1, false>(p, st);
     return groups <= cus ? rows_of<1, 1, false>(p, st) : rows_of<1, 2, false>(p, st);
   }
-  const int64_t cost[5] = {r0 == 1 ? 36 : 50 * r0x2, 43 * rounds(64, 128, cus),
-                           63 * rounds(128, 128, cus), 98 * rounds(128, 256, cus),
-                           175 * rounds(256, 256, cus)};
-  switch (std::min_element(cost, cost + 5) - cost) {
+  if (by_32 < by_tile) return tile_launch<1, 1, 2, 2, 3, false, 4>(p, st);
+  switch (best) {
     case 0: return tile_launch<2, 2, 2, 2, 4, false>(p, st);
     case 1: return tile_launch<2, 4, 2, 2, 4, false>(p, st);
     case 2: return tile_launch<2, 4, 4, 2, 2, false>(p, st);

@@ -588,3 +588,35 @@ def test_gemm_many_rows_of_few_columns():
     """Straight from memory at many rows: the scales' offsets, and K of many blocks."""
     test_gemm_whole_numbers_exactly(5512, 352, 24, 1)
     test_gemm_whole_numbers_exactly(1463, 4016, 40, 1)
+
+
+# 32 x 32 tiles, whose stages hold four blocks of K: K that ends inside a stage and inside a block.
+GEMM_PARTS = [(60, 4112, 4040, 1), (97, 6160, 1032, 2), (40, 5008, 3592, 1), (130, 3600, 1544, 1),
+              (1040, 4240, 200, 1), (20, 8336, 7000, 1), (33, 2576, 3528, 1), (64, 6032, 1032, 3)]
+
+
+@pytest.mark.parametrize("M,K,Ns,S", GEMM_PARTS)
+def test_gemm_parts(M, K, Ns, S):
+    test_gemm(M, K, Ns, S)
+
+
+@pytest.mark.parametrize("M,K,Ns,S", GEMM_PARTS)
+def test_gemm_parts_whole_numbers_exactly(M, K, Ns, S):
+    test_gemm_whole_numbers_exactly(M, K, Ns, S)
+
+
+@pytest.mark.parametrize("M,K,Ns", [(3, 272, 264), (60, 4112, 4040), (33, 2576, 3528), (300, 1168, 2056)])
+def test_gemm_infinite_scales_of_columns_stay_there(M, K, Ns):
+    """The scale behind a column block's last one is the next block's first."""
+    g = gen(M)
+    xq, xs = fr.whole_rows(g, M, K)
+    wq, ws = fr.whole_weights(g, 1, Ns, K)
+    ws[0, 1, 0] = float("inf")
+    ws[0, -1, 0] = float("nan")
+    y = mla.moe_lora_fp8_gemm(_rows(xq, xs), wq.to(DEV), ws.to(DEV)).cpu()
+    keep = torch.ones(Ns, dtype=torch.bool)
+    keep[128:256] = keep[(Ns - 1) // 128 * 128:] = False
+    ws[~torch.isfinite(ws)] = 1.0
+    ref, _ = fr.gemm(xq, xs, wq, ws)
+    assert torch.equal(y[:, keep], ref[:, keep].float().to(BF))
+    assert not bool(torch.isfinite(y[:, ~keep]).any())
