@@ -61,17 +61,17 @@ __device__ __forceinline__ RowMap row_of(const GemmParams& p, int64_t first, int
 }
 
 // ---------------------------------------------------------------- few rows
-// One workgroup computes 16 MT rows x 16 NT columns: its KW wavefronts take
-// the K blocks w, w + KW, ... straight from memory (together they read KW x 128
+// One workgroup computes 16 MT rows x 16 NT columns: its kSplit wavefronts take
+// the K blocks w, w + kSplit, ... straight from memory (together they read kSplit x 128
 // consecutive bytes of each row of W) and add their sums in LDS, in order.
 // Bound by the stream of W: 20b-like decode w13 (64 pairs, 464 MB) 81 us, 5.7
 // TB/s, with a wavefront's loads of one block ahead of its products; two blocks
 // ahead 83 us.  Grouped, the workgroups of a block take its pieces of 16 rows in
 // steps of `step` rows.
-constexpr int KW = 8;
+constexpr int kSplit = 8;
 template <int MT, int NT, bool GROUPED>
-__global__ void __launch_bounds__(KW * kWave) fp8_gemm_rows_kernel(GemmParams p, int ntiles, int step) {
-  __shared__ f32x4_t red[KW][MT * NT][kWave];
+__global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParams p, int ntiles, int step) {
+  __shared__ f32x4_t red[kSplit][MT * NT][kWave];
   const int tile = blockIdx.x % (p.S * ntiles);
   int64_t first = int64_t(blockIdx.x / (p.S * ntiles)) * 16 * MT, stop = 0;
   int64_t e = 0;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(KW * kWave) fp8_gemm_rows_kernel(GemmParams p,
 #pragma unroll
       for (int f = 0; f < NT; ++f) acc[i][f] = f32x4_t{0, 0, 0, 0};
 
-    for (int kb = w; kb < p.KB; kb += KW) {
+    for (int kb = w; kb < p.KB; kb += kSplit) {
       const uint32_t k = uint32_t(kb) * kScaleBlock;
       const uint32_t lo = k + 16 * g < uint32_t(p.K) ? k : kOob;
       const uint32_t hi = k + 64 + 16 * g < uint32_t(p.K) ? k + 64 : kOob;
@@ -155,11 +155,11 @@ __global__ void __launch_bounds__(KW * kWave) fp8_gemm_rows_kernel(GemmParams p,
 #pragma unroll
       for (int f = 0; f < NT; ++f) red[w][i * NT + f][lane] = acc[i][f];
     __syncthreads();
-    for (int t = w; t < MT * NT; t += KW) {
+    for (int t = w; t < MT * NT; t += kSplit) {
       const int i = t / NT, f = t % NT;
       f32x4_t s = red[0][t][lane];
 #pragma unroll
-      for (int v = 1; v < KW; ++v) s += red[v][t][lane];
+      for (int v = 1; v < kSplit; ++v) s += red[v][t][lane];
       const RowMap r = row_of<GROUPED>(p, first, 16 * i + a);
       const int n = n0 + 16 * f + 4 * g;
       if (r.y_row < 0 || n >= p.Ns) continue;
@@ -753,7 +753,7 @@ hipError_t rows_of(const GemmParams& p, hipStream_t st) {
   const int ntiles = (p.Ns + 16 * NT - 1) / (16 * NT);
   const int64_t grid = rows_grid<MT, NT, GROUPED>(p);
   hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, NT, GROUPED>), dim3(unsigned(grid)),
-                     dim3(KW * kWave), 0, st, p, ntiles, GROUPED ? int(parts_of<MT>(p)) * 16 * MT : 0);
+                     dim3(kSplit * kWave), 0, st, p, ntiles, GROUPED ? int(parts_of<MT>(p)) * 16 * MT : 0);
   return hipGetLastError();
 }
 
