@@ -63,14 +63,29 @@ __device__ __forceinline__ float amax8(const float (&f)[8]) {
 // Scale of a block from its largest magnitude: the division is the IEEE one.
 __device__ __forceinline__ float block_scale(float amax) { return fmaxf(amax, kMinAmax) / kE4m3Max; }
 
-// 8 values over the scale, rounded once to e4m3 (nearest even).  |v| * inv is
-// at most 448 (1 + 2^-22), which rounds to 448: the conversion never overflows
-// on finite values.  An infinite block has inv = 0: its infinities become NaN.
-__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0] * inv, f[1] * inv, 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2] * inv, f[3] * inv, lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4] * inv, f[5] * inv, 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6] * inv, f[7] * inv, hi, true);
+// 8 values over the scale, each quotient rounded to fp32 as a division does and
+// then to e4m3, nearest even.  Values and scale come from few bits, so quotients
+// often lie halfway between two e4m3 values; times the rounded reciprocal alone
+// some of them would go the other way.  One step on the remainder gives the
+// division's quotient (P. Markstein, IBM J. Res. Dev. 34, 1990; no difference in
+// 2e7 sampled quotients above 2^-11, smaller ones round to 0 either way).  8192 x
+// 1024 without residual: 9.1 us, with the compiler's divisions 10.6, with the
+// reciprocal alone 9.0; 16384 x 4096 101.4 with each of them.
+// |v| / scale is at most 448 (1 + 2^-23), which rounds to 448: the conversion never
+// overflows on finite values.  In an infinite block the reciprocal is 0: finite
+// values become 0 and infinities NaN.
+__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float s) {
+  const float inv = 1.0f / s, finite = fminf(s, 0x1.fffffep127f);  // (0 times infinity is NaN)
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = f[i] * inv;
+    q[i] = fmaf(fmaf(-q[i], finite, f[i]), inv, q[i]);
+  }
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
   return make_uint2(uint32_t(lo), uint32_t(hi));
 }
 
@@ -132,7 +147,7 @@ __global__ void __launch_bounds__(T) rms_norm_fp8_kernel(NormParams p) {
     const float s = block_scale(row16_max(amax));
     if (c < nc) {
       if (p.y) store16(p.y + row * p.H + 8 * c, pack8(v[i]));
-      store8(p.q + row * p.H + 8 * c, quantise8(v[i], 1.0f / s));
+      store8(p.q + row * p.H + 8 * c, quantise8(v[i], s));
       if ((c & 15) == 0) p.scales[int64_t(c >> 4) * p.M + row] = s;
     }
   }
@@ -163,7 +178,7 @@ __global__ void __launch_bounds__(kTS) silu_mul_fp8_kernel(SiluParams p, int32_t
     const float s = block_scale(row16_max(amax));
     if (in) {
       if (p.h) store16(p.h + row * p.I + col, pack8(v));
-      store8(p.q + row * p.I + col, quantise8(v, 1.0f / s));
+      store8(p.q + row * p.I + col, quantise8(v, s));
       if (sub == 0) p.scales[int64_t(j) * p.P + row] = s;
     }
   }

@@ -1,0 +1,52 @@
+"""The 8-bit base side where its definition decides: roundings on exact ties, the largest launches,
+buffers of other streams, and ids outside their range."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import moe_lora_adapter_amd as mla  # noqa: E402
+import fp8_reference as fr  # noqa: E402
+import gpu_helpers as gh  # noqa: E402
+
+DEV, BF = gh.DEV, torch.bfloat16
+
+
+# ---------------------------------------------------------------- rounding
+# Inputs whose fp32 value is known to the last bit, so that the scales and the e4m3 values follow
+# from the definition exactly: scale = max(2^-40, largest) / 448, q = e4m3(value / scale), the two
+# quotients rounded to fp32.  bf16 values over a bf16 maximum meet ties between two e4m3 values;
+# a product with the reciprocal breaks some of them the other way.
+
+def _rows_exactly(out, v):
+    """Returns in how many places the reciprocal's product would differ."""
+    K = v.shape[1]
+    s = torch.stack([v[:, k:k + 128].abs().max(1).values.clamp(min=fr.MIN_AMAX) / fr.F8_MAX
+                     for k in range(0, K, 128)])
+    wide = s.t().repeat_interleave(128, 1)[:, :K]
+    q = (v / wide).to(fr.F8).view(torch.uint8)
+    assert torch.equal(out.scales.cpu(), s)
+    assert torch.equal(out.q.cpu().view(torch.uint8), q)
+    return int((q != (v * (1.0 / wide)).to(fr.F8).view(torch.uint8)).sum())
+
+
+@pytest.mark.parametrize("H,weights", [(1024, 16), (2048, 2), (4096, 2), (8192, 2), (65528, 1)])
+def test_rms_norm_rounds_the_quotient(H, weights):
+    """x = +-2 in every place: the mean of the squares is 4 and the norm +-1 times the weight."""
+    g, differ = torch.Generator().manual_seed(H), 0
+    for _ in range(weights):
+        x = (2.0 * (2 * torch.randint(0, 2, (5, H), generator=g) - 1)).to(BF)
+        w = torch.randn(H, generator=g).to(BF)
+        out = mla.moe_lora_rms_norm_fp8(x.to(DEV), w.to(DEV), eps=0.0)
+        differ += _rows_exactly(out, x.float() * 0.5 * w.float())
+    assert differ > 0, "the case does not tell the two apart"
+
+
+@pytest.mark.parametrize("P,I", [(300, 136), (64, 1160), (33, 2880)])
+def test_silu_mul_rounds_the_quotient(P, I):
+    """silu(64) is 64 in fp32."""
+    u = torch.randn((P, I), generator=torch.Generator().manual_seed(I)).to(BF)
+    y = torch.cat([torch.full_like(u, 64.0), u], 1)
+    differ = _rows_exactly(mla.moe_lora_silu_mul_fp8(y.to(DEV)), 64.0 * u.float())
+    assert differ > 0, "the case does not tell the two apart"
