@@ -748,6 +748,10 @@ int64_t rows_grid(const GemmParams& p) {
   return pieces * p.S * ((p.Ns + 16 * NT - 1) / (16 * NT));
 }
 
+// Whether one launch takes so many workgroups of the rows kernel: it has fewer
+// than 2^32 threads.  (The tiles' workgroups go from tile to tile, any number.)
+bool rows_fit(int64_t grid) { return grid < (int64_t(1) << 32) / (kSplit * kWave); }
+
 template <int MT, int NT, bool GROUPED>
 hipError_t rows_of(const GemmParams& p, hipStream_t st) {
   const int ntiles = (p.Ns + 16 * NT - 1) / (16 * NT);
@@ -789,7 +793,10 @@ hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
                                                      (p.M <= 16 ? 8e-4 : 1.6e-3) * double(groups * passes));
   const double by_32 = once32 ? 3.5 + 1.4e-3 * p.K : INFINITY;
   const double by_tile = 3 + 0.01 * p.KB * double(cost[best]);
-  if (by_rows < std::min(by_32, by_tile)) {
+  const int64_t grid = p.M > 16         ? rows_grid<2, 1, false>(p)
+                       : groups <= cus ? rows_grid<1, 1, false>(p)
+                                       : rows_grid<1, 2, false>(p);
+  if (by_rows < std::min(by_32, by_tile) && rows_fit(grid)) {
     // (16 rows: up to a CU's worth of groups of 16 columns 6.1 us, in 32s 7.8, 4096
     // x 4096; beyond, 2880 x 5120, 6.0 and 4.9)
     if (p.M > 16) return rows_of<2, 1, false>(p, st);
@@ -822,9 +829,7 @@ hipError_t launch_fp8_moe_gemm(GemmParams p, hipStream_t st) {
   const double groups = double(p.S) * ((p.Ns + 31) / 32);
   const double by_rows = 3 + double(tiles(16)) * std::max(stream, 0.004 * groups);
   const double by_tiles = 10 + std::max(0.45 * p.KB, 0.2 * p.KB + double(used) * stream);
-  // (a launch has fewer than 2^32 threads)
-  const bool fits = rows_grid<1, 2, true>(p) < (int64_t(1) << 32) / (8 * kWave);
-  if (by_rows <= by_tiles && fits) {
+  if (by_rows <= by_tiles && rows_fit(rows_grid<1, 2, true>(p))) {
     // 64 columns a workgroup read X half as often as 32, which is worth it from a
     // few rows an expert on and with a workgroup for every CU (64 experts of 1024
     // x 4096: 1 row each 36.3 us and 32.7, 8 rows 52.3 and 53.7; 128 of 2880 x

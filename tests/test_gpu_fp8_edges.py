@@ -50,3 +50,25 @@ def test_silu_mul_rounds_the_quotient(P, I):
     y = torch.cat([torch.full_like(u, 64.0), u], 1)
     differ = _rows_exactly(mla.moe_lora_silu_mul_fp8(y.to(DEV)), 64.0 * u.float())
     assert differ > 0, "the case does not tell the two apart"
+
+
+# ---------------------------------------------------------------- launches
+
+@pytest.mark.parametrize("M,K,Ns,S", [(1, 16, 8, 1 << 23), (300, 512, 8, 1 << 20)])
+def test_gemm_more_slices_than_one_launch_of_few_rows_takes(M, K, Ns, S):
+    """2^23 workgroups of 512 threads are 2^32 threads, which no launch has.  Whole numbers, every
+    sum a multiple of 1/4 below 2^15: exact in fp32 in any order."""
+    g = torch.Generator(device=DEV).manual_seed(S)
+    whole = lambda *s: torch.randint(-4, 5, s, device=DEV, generator=g).float()  # noqa: E731
+    x, w = whole(M, K), torch.empty((S, Ns, K), dtype=fr.F8, device=DEV)
+    step = S // 16
+    for i in range(0, S, step):
+        w[i:i + step] = whole(step, Ns, K).to(fr.F8)
+    xs = 2.0 ** torch.randint(-1, 2, (fr.blocks(K), M), device=DEV, generator=g).float()
+    ws = 2.0 ** torch.randint(-1, 2, (S, 1, fr.blocks(K)), device=DEV, generator=g).float()
+    y = mla.moe_lora_fp8_gemm(mla.Fp8Rows(x.to(fr.F8), xs), w, ws)
+    wide = x * xs.t().repeat_interleave(128, 1)[:, :K]
+    for i in range(0, S, step):
+        wf = w[i:i + step].float() * ws[i:i + step].repeat_interleave(128, 2)[:, :, :K]
+        want = (wide @ wf.view(step * Ns, K).t().contiguous()).to(BF)
+        assert torch.equal(y[:, i * Ns:(i + step) * Ns], want)
