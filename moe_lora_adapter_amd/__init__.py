@@ -19,6 +19,7 @@ The 8-bit base side of the same layer:
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -166,6 +167,18 @@ def _stream_ptr(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+_TAKEN_HERE = contextlib.nullcontext()
+
+
+def _taken_on(stream):
+    """Context in which a call allocates its own buffers: the allocator orders a buffer's uses by
+    the stream it was taken on, which has to be the one the call writes it on."""
+    if stream is None:
+        return _TAKEN_HERE
+    import torch
+    return torch.cuda.stream(stream)
 
 
 def _check(t, name, dtype, device):
@@ -483,7 +496,8 @@ def _direct(torch, device, stream):
 def moe_lora_rms_norm_fp8(x, weight, *, eps: float = 1e-6, residual=None, residual_out=None, y=None,
                           out: Fp8Rows | None = None, stream=None) -> Fp8Rows:
     """RMS norm of x (+ residual) as 8-bit rows, and as bf16 in y when given; the sum goes to
-    residual_out (None: in place on residual); see moe_lora.h."""
+    residual_out (None: in place on residual); see moe_lora.h.  Buffers that a call allocates are
+    of the stream it runs on."""
     import torch
     bf = torch.bfloat16
     if not isinstance(x, torch.Tensor) or x.dtype is not bf or not x.is_contiguous():
@@ -494,7 +508,8 @@ def moe_lora_rms_norm_fp8(x, weight, *, eps: float = 1e-6, residual=None, residu
     M, H = shape
     at = x.get_device()
     if out is None:
-        out = alloc_fp8_rows(M, H, x.device)
+        with _taken_on(stream):
+            out = alloc_fp8_rows(M, H, x.device)
     if (weight.dtype is not bf or weight.shape != (H,) or not weight.is_contiguous()
             or weight.get_device() != at):
         _refuse(weight, "weight", bf, x.device, (H,))
@@ -561,7 +576,8 @@ def moe_lora_silu_mul_fp8(y, *, h=None, out: Fp8Rows | None = None, stream=None)
             _refuse(h, "h", bf, y.device, (P, I))
         ph = h.data_ptr()
     if out is None:
-        out = alloc_fp8_rows(P, I, y.device)
+        with _taken_on(stream):
+            out = alloc_fp8_rows(P, I, y.device)
     pq, ps = _rows_ptrs(torch, out, "out", P, I, y, at)
     raw = _direct(torch, at, stream)
     if raw is None:
@@ -596,7 +612,8 @@ def moe_lora_fp8_gemm(x: Fp8Rows, w, w_scales, y=None, *, stream=None):
     pw, pws = _weight_ptrs(torch, w, w_scales, shape, at)
     pq, ps = _rows_ptrs(torch, x, "x", M, K, w, at)
     if y is None:
-        y = torch.empty((M, S * Ns), dtype=torch.bfloat16, device=w.device)
+        with _taken_on(stream):
+            y = torch.empty((M, S * Ns), dtype=torch.bfloat16, device=w.device)
     elif (y.dtype is not torch.bfloat16 or y.shape != (M, S * Ns) or not y.is_contiguous()
           or y.get_device() != at):
         _refuse(y, "y", torch.bfloat16, w.device, (M, S * Ns))

@@ -72,3 +72,38 @@ def test_gemm_more_slices_than_one_launch_of_few_rows_takes(M, K, Ns, S):
         wf = w[i:i + step].float() * ws[i:i + step].repeat_interleave(128, 2)[:, :, :K]
         want = (wide @ wf.view(step * Ns, K).t().contiguous()).to(BF)
         assert torch.equal(y[:, i * Ns:(i + step) * Ns], want)
+
+
+# ---------------------------------------------------------------- streams
+
+def _stream_of(t):
+    """The stream that the allocator gave a tensor's memory to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's")
+
+
+def test_buffers_of_a_call_on_a_given_stream_are_that_streams():
+    """A buffer that a call allocates is taken from the stream that the call writes it on: memory
+    that work of the current stream may still be using, or is given next, is another."""
+    g = torch.Generator().manual_seed(9)
+    xb, w = torch.randn((40, 272), generator=g).to(BF).to(DEV), torch.ones(272, dtype=BF, device=DEV)
+    wq, ws = fr.rand_weights(g, 1, 136, 272)
+    wq, ws = wq.to(DEV), ws.to(DEV)
+    want = mla.moe_lora_rms_norm_fp8(xb, w)
+    want_h = mla.moe_lora_silu_mul_fp8(xb)
+    want_y = mla.moe_lora_fp8_gemm(want, wq, ws)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    n = mla.moe_lora_rms_norm_fp8(xb, w, stream=s)
+    h = mla.moe_lora_silu_mul_fp8(xb, stream=s)
+    y = mla.moe_lora_fp8_gemm(n, wq, ws, stream=s)
+    s.synchronize()
+    for t in (n.q, n.scales, h.q, h.scales, y):
+        assert _stream_of(t) == s.cuda_stream
+    for a, b in ((n.q, want.q), (h.q, want_h.q)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(n.scales, want.scales) and torch.equal(h.scales, want_h.scales)
+    assert torch.equal(y.view(torch.int16), want_y.view(torch.int16))
+    assert torch.cuda.current_stream() != s
