@@ -212,11 +212,12 @@ def moe_lora_align(topk_ids, token_lora_mapping, E: int, L: int, block_m: int, *
     if topk_ids.dim() != 2 or token_lora_mapping.shape != (topk_ids.shape[0],):
         raise ValueError("topk_ids must be [M, topk] and token_lora_mapping [M]")
     M, topk = topk_ids.shape
-    if out is None:
-        out = alloc_align_output(M, topk, E, L, block_m, dev)
-    ws_bytes = align_workspace_size(M, topk, E, L, block_m)
-    if ws_bytes > 0 and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    with _taken_on(stream):
+        if out is None:
+            out = alloc_align_output(M, topk, E, L, block_m, dev)
+        ws_bytes = align_workspace_size(M, topk, E, L, block_m)
+        if ws_bytes > 0 and workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     rc = lib().moe_lora_align(
         _dptr(topk_ids), _dptr(token_lora_mapping), M, topk, E, L, block_m,
         _dptr(out.sorted_token_ids), _dptr(out.expert_ids), _dptr(out.num_tokens_post_padded),
@@ -360,7 +361,8 @@ def fused_moe_lora_with_align(topk_ids, token_lora_mapping, x, lora_a, lora_b, t
     if tuple(topk_ids.shape) != (M, topk) or tuple(token_lora_mapping.shape) != (M,):
         raise ValueError("topk_ids must be [M, topk] and token_lora_mapping [M]")
     if out is None:
-        out = alloc_align_output(M, topk, E, L, block_m, y.device)
+        with _taken_on(stream):
+            out = alloc_align_output(M, topk, E, L, block_m, y.device)
     rc = lib().fused_moe_lora_with_align(
         _dptr(topk_ids), _dptr(token_lora_mapping), M, topk, E, L, block_m,
         _dptr(out.sorted_token_ids), _dptr(out.expert_ids), _dptr(out.num_tokens_post_padded),
@@ -413,7 +415,8 @@ def fused_moe_lora_two_kernel(x, lora_a, lora_b, align: AlignOutput, topk_weight
         raise ValueError("align output was made for another L")
     nbytes = two_kernel_workspace_bytes(M, topk, K, Ns, S, E, L, r, align.block_m, x_per_pair)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=y.device)
+        with _taken_on(stream):
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=y.device)
     _check(workspace, "workspace", workspace.dtype, y.device)
     rc = lib().fused_moe_lora_two_kernel(
         _dptr(x), int(bool(x_per_pair)), _dptr(lora_a), _dptr(lora_b),
