@@ -48,12 +48,14 @@ struct RowMap {
   int64_t x_row;  // row of X, or -1
   int64_t y_row;  // row of Y, or -1
 };
+__device__ __forceinline__ RowMap row_of_pair(const GemmParams& p, uint32_t pair) {
+  if (pair >= uint32_t(p.numel)) return {-1, -1};
+  return {int64_t(p.x_per_pair ? pair : pair / uint32_t(p.topk)), int64_t(pair)};
+}
 template <bool GROUPED>
 __device__ __forceinline__ RowMap row_of(const GemmParams& p, int64_t first, int i) {
   if constexpr (GROUPED) {
-    const uint32_t pair = uint32_t(p.sorted[first + i]);
-    if (pair >= uint32_t(p.numel)) return {-1, -1};
-    return {int64_t(p.x_per_pair ? pair : pair / uint32_t(p.topk)), int64_t(pair)};
+    return row_of_pair(p, uint32_t(p.sorted[first + i]));
   } else {
     const int64_t r = first + i;
     return r < p.M ? RowMap{r, r} : RowMap{-1, -1};
@@ -73,20 +75,45 @@ template <int MT, int NT, bool GROUPED>
 __global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParams p, int ntiles, int step) {
   __shared__ f32x4_t red[kSplit][MT * NT][kWave];
   const int tile = blockIdx.x % (p.S * ntiles);
-  int64_t first = int64_t(blockIdx.x / (p.S * ntiles)) * 16 * MT, stop = 0;
-  int64_t e = 0;
-  if constexpr (GROUPED) {
-    const int q = blockIdx.x / (p.S * ntiles), block = q % p.blocks;
-    first = int64_t(block) * p.block_m + q / p.blocks * (16 * MT);
-    stop = int64_t(block + 1) * p.block_m;
-    // a block's pairs come first, its padding last: pieces of padding end here
-    // (what is behind the last block is read too, in one wait, and not used)
-    const int32_t used = p.ntpp[0], lead = p.sorted[first];
-    e = p.eids[block];
-    if (first >= used || uint32_t(lead) >= uint32_t(p.numel) || e < 0 || e >= p.E) return;
-  }
   const int slice = tile / ntiles, n0 = (tile % ntiles) * 16 * NT;
   const int lane = lane_id(), w = wave_id(), a = lane & 15, g = lane >> 4;
+  int64_t first = int64_t(blockIdx.x / (p.S * ntiles)) * 16 * MT, start = 0, stop = 0;
+  int64_t e = 0;
+  // grouped: the block's ids, one or two a lane, and which of them are a pair's
+  int32_t id0 = -1, id1 = -1;
+  uint64_t held0 = 0, held1 = 0;
+  // the first piece from `first` on, in this workgroup's steps, that has one
+  auto seek = [&]() {
+    for (; first < stop; first += step) {
+      const int at = int(first - start);
+      if ((at < kWave ? held0 : held1) >> (at % kWave) & ((uint64_t(1) << 16 * MT) - 1)) return;
+    }
+  };
+  // row i of the piece
+  auto row_at = [&](int i) {
+    if constexpr (GROUPED) {
+      const int at = int(first - start);
+      return row_of_pair(p, uint32_t(__shfl(at < kWave ? id0 : id1, at % kWave + i)));
+    } else {
+      return row_of<false>(p, first, i);
+    }
+  };
+  if constexpr (GROUPED) {
+    const int q = blockIdx.x / (p.S * ntiles), block = q % p.blocks;
+    start = int64_t(block) * p.block_m;
+    first = start + q / p.blocks * (16 * MT);
+    stop = start + p.block_m;
+    // (what is behind the last block is read too, in one wait, and not used)
+    const int32_t used = p.ntpp[0];
+    if (lane < p.block_m) id0 = p.sorted[start + lane];
+    if (kWave + lane < p.block_m) id1 = p.sorted[start + kWave + lane];
+    e = p.eids[block];
+    held0 = __ballot(uint32_t(id0) < uint32_t(p.numel));
+    held1 = __ballot(uint32_t(id1) < uint32_t(p.numel));
+    if (start >= used || e < 0 || e >= p.E) return;
+    seek();
+    if (first >= stop) return;  // padding
+  }
 
   const uint8_t* wbase = p.w + (e * p.S + slice) * p.Ns * int64_t(p.K);
   const auto wr = make_rsrc(wbase, uint32_t(p.Ns) * uint32_t(p.K));
@@ -100,8 +127,7 @@ __global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParam
     const int n = n0 + 16 * f + a;
     woff[f] = n < p.Ns ? uint32_t(n) * uint32_t(p.K) + 16 * g : kOob;
   }
-  for (bool more = true; more;) {
-    more = GROUPED && first + step < stop && uint32_t(p.sorted[first + step]) < uint32_t(p.numel);
+  for (;;) {
     // rows of X: dense tiles are addressed from their first row, grouped ones
     // from row 0 (X is below 2 GiB there)
     const int64_t x0 = GROUPED ? 0 : first;
@@ -111,7 +137,7 @@ __global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParam
     uint32_t xoff[MT], soff[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const RowMap r = row_of<GROUPED>(p, first, 16 * i + a);
+      const RowMap r = row_at(16 * i + a);
       xoff[i] = r.x_row >= 0 ? uint32_t((r.x_row - x0) * p.K) + 16 * g : kOob;
       soff[i] = r.x_row >= 0 ? uint32_t(r.x_row) * 4 : kOob;
     }
@@ -160,7 +186,7 @@ __global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParam
       f32x4_t s = red[0][t][lane];
 #pragma unroll
       for (int v = 1; v < kSplit; ++v) s += red[v][t][lane];
-      const RowMap r = row_of<GROUPED>(p, first, 16 * i + a);
+      const RowMap r = row_at(16 * i + a);
       const int n = n0 + 16 * f + 4 * g;
       if (r.y_row < 0 || n >= p.Ns) continue;
       if constexpr (GROUPED) {
@@ -169,8 +195,11 @@ __global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParam
       uint2 o = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
       *reinterpret_cast<uint2*>(p.y + r.y_row * (int64_t(p.S) * p.Ns) + slice * p.Ns + n) = o;
     }
+    if constexpr (!GROUPED) return;
     first += step;
-    if (more) __syncthreads();  // the sums have been read
+    seek();
+    if (first >= stop) return;
+    __syncthreads();  // the sums have been read
   }
 }
 
@@ -551,11 +580,15 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
     uint32_t row, tile;
     items.at(ct, &row, &tile);
     const int slice = tile / ntiles, n0 = (tile % ntiles) * BN;
-    // A wavefront without a row or a column of the tile (its rows come first,
-    // what is missing last) only loads and keeps the barriers.
+    // A wavefront without a row or a column of the tile only loads and keeps the
+    // barriers.
     bool none = n0 + wn * FN * 16 >= p.Ns;
     if constexpr (GROUPED) {
-      none |= __builtin_amdgcn_readfirstlane(pairs[ring * BM + wm * FM * 16].x) < 0;
+      constexpr int kRows = FM * 16;
+      const int2* own = pairs + ring * BM + wm * kRows;
+      bool row = own[lane % kRows].x >= 0;
+      if constexpr (kRows > kWave) row |= own[kWave + lane].x >= 0;
+      none |= __ballot(row) == 0;
     } else {
       none |= int64_t(row) * BM + wm * FM * 16 >= p.M;
     }

@@ -1,5 +1,6 @@
 """The 8-bit base side where its definition decides: roundings on exact ties, the largest launches,
 buffers of other streams, and ids outside their range."""
+import numpy as np
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -107,3 +108,64 @@ def test_buffers_of_a_call_on_a_given_stream_are_that_streams():
     assert torch.equal(n.scales, want.scales) and torch.equal(h.scales, want_h.scales)
     assert torch.equal(y.view(torch.int16), want_y.view(torch.int16))
     assert torch.cuda.current_stream() != s
+
+
+# ---------------------------------------------------------------- ids outside their range
+
+def _mask(ids, B, used, kind):
+    """`ids` (one slot's sorted pairs) with some taken out, wherever in a block they stand."""
+    at = torch.arange(used)
+    gone = {"first of a block": at % B == 0,
+            "first of 16": at % 16 == 0,
+            "first 16 of a block": at % B < 16,
+            "all but the last of 16": at % 16 != 15,
+            "every third": at % 3 == 1,
+            "all but the last of a block": at % B != B - 1}[kind]
+    out = ids.clone()
+    bad = torch.tensor([-1, 1 << 30, -(1 << 31)], dtype=torch.int32)
+    out[:used][gone] = bad[torch.arange(int(gone.sum())) % 3]
+    return out
+
+
+KINDS = ["first of a block", "first of 16", "first 16 of a block", "all but the last of 16",
+         "every third", "all but the last of a block"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,topk,K,Ns,S,E,B,per_pair", [
+    (60, 2, 272, 136, 1, 4, 16, False),        # few rows, 32 columns
+    (200, 2, 272, 136, 1, 16, 128, True),      # the same, pieces of a block in turn
+    (600, 1, 144, 72, 1, 3, 64, False),        # the same, several of them at once
+    (90, 2, 272, 2056, 1, 8, 128, False),      # few rows, 64 columns
+    (400, 8, 272, 1288, 1, 64, 16, False),     # tiles of 64 rows
+    (700, 2, 1168, 520, 2, 7, 32, True),
+    (700, 2, 1168, 520, 2, 7, 128, True),      # tiles of 128 rows
+    (1000, 4, 784, 1544, 1, 3, 32, False),
+    (900, 8, 64, 1544, 1, 64, 128, False),     # tiles of 256 rows
+    (2500, 4, 128, 1032, 1, 64, 64, True)])
+def test_moe_gemm_passes_over_pairs_outside_their_range(M, topk, K, Ns, S, E, B, per_pair, kind):
+    """Ids that are no pair's, anywhere in a block: the others' rows are computed, and no more."""
+    rng, g = np.random.default_rng(M + K), torch.Generator().manual_seed(M)
+    ids = rng.integers(0, E, (M, topk)).astype(np.int32)
+    xq, xs = fr.whole_rows(g, M * topk if per_pair else M, K)
+    wq, ws = fr.whole_weights(g, E, S, Ns, K)
+    tw = 2.0 ** torch.randint(-2, 3, (M, topk), generator=g).float()
+    al = mla.moe_lora_align(gh.i32_dev(ids), torch.zeros(M, dtype=torch.int32, device=DEV), E, 1, B)
+    used = int(al.num_tokens_post_padded.item())
+    kept = _mask(al.sorted_token_ids[0].cpu(), B, used, kind)
+    al.sorted_token_ids[0].copy_(kept)
+    x, w, sc, dw = mla.Fp8Rows(xq.to(DEV), xs.to(DEV)), wq.to(DEV), ws.to(DEV), tw.to(DEV)
+    y = torch.full((M, topk, S * Ns), 5.0, dtype=BF, device=DEV)
+    mla.moe_lora_fp8_moe_gemm(x, w, sc, al, dw, y, mul_routed_weight=True, x_per_pair=per_pair)
+    want = torch.full((M * topk, S * Ns), 5.0, dtype=BF, device=DEV)
+    xw = fr.widen_rows(xq, xs).float().to(DEV)
+    left = kept[:used]
+    left = left[(left >= 0) & (left < M * topk)].long().to(DEV)
+    flat, wt = gh.i32_dev(ids).view(-1), dw.view(-1)
+    for e in range(E):
+        p = left[flat[left] == e]
+        if p.numel():
+            d = xw[p if per_pair else p // topk] @ fr.widen_weights(wq[e], ws[e]).float().view(
+                S * Ns, K).to(DEV).t().contiguous()
+            want[p] = (d * wt[p][:, None]).to(BF)
+    assert torch.equal(y.view(M * topk, S * Ns), want)
