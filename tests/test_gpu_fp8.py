@@ -143,8 +143,9 @@ def test_gemm_whole_numbers_exactly(M, K, Ns, S):
     assert torch.equal(y, ref.float().to(BF))
 
 
-# More tiles than the device holds at once, so that a workgroup takes several: each tile size, K of
-# one block, of two and of more than the ring's stages, tiles that end in the last row and column.
+# More tiles than the device holds at once, so that a workgroup takes several: tiles of 64 x 128 and
+# larger, K of one block, of two and of more than the ring's stages, tiles that end in the last row
+# and column.
 MANY = [(4100, 64, 5000, 1), (4100, 144, 4104, 1), (5000, 400, 4304, 2), (3000, 272, 9000, 1),
         (4096, 1040, 8200, 1), (2000, 528, 4104, 1), (700, 400, 4200, 2), (1500, 128, 12304, 1),
         (65, 272, 40000, 1), (130, 656, 33000, 1), (64, 272, 70000, 1), (12000, 272, 264, 1),
