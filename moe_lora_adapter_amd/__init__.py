@@ -487,9 +487,14 @@ def _call(name, x, stream, *args):
 
 def _direct(torch, device, stream):
     """The raw current stream when nothing has to be switched for a call on `device`, else None:
-    making a Stream object costs more than the call."""
-    if stream is None and device >= 0 and torch._C._cuda_getDevice() == device:
-        return torch._C._cuda_getCurrentRawStream(device)
+    making a Stream object costs more than the call.  The two names are not torch's public ones;
+    where they are missing the calls go through _call."""
+    if stream is None and device >= 0:
+        try:
+            if torch._C._cuda_getDevice() == device:
+                return torch._C._cuda_getCurrentRawStream(device)
+        except AttributeError:
+            pass
     return None
 
 
