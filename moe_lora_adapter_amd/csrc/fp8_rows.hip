@@ -155,7 +155,10 @@ __global__ void __launch_bounds__(T) rms_norm_fp8_kernel(NormParams p) {
 
 // 16 lanes a (row, block of 128 columns); a workgroup takes the same block of 16
 // consecutive rows, whose scales are neighbours.  65536 x 768 (7 bytes a value): 62
-// us, 5.7 TB/s; 64 workgroups a CU, 16 of them took 66 us.
+// us, 5.7 TB/s; 64 workgroups a CU, 16 of them took 66 us.  The exponential is the
+// hardware's power of two of a rounded argument: off by some |g| 2^-24 of its
+// value, 2^-17 at most where it counts, against bf16's 2^-8 and e4m3's 2^-4 at the
+// output (the library's exact one: 4096 x 2880 18.7 us, so 17.6).
 constexpr int kTS = 256, kRows = kTS / 16;
 __global__ void __launch_bounds__(kTS) silu_mul_fp8_kernel(SiluParams p, int32_t nb, int64_t items) {
   const int sub = threadIdx.x & 15;
