@@ -66,53 +66,56 @@ __device__ __forceinline__ RowMap row_of(const GemmParams& p, int64_t first, int
 // One workgroup computes 16 MT rows x 16 NT columns: its kSplit wavefronts take
 // the K blocks w, w + kSplit, ... straight from memory (together they read kSplit x 128
 // consecutive bytes of each row of W) and add their sums in LDS, in order.
-// Bound by the stream of W: 20b-like decode w13 (64 pairs, 464 MB) 81 us, 5.7
+// Bound by the stream of W: 20b-like decode w13 (64 pairs, 464 MB) 79 us, 5.9
 // TB/s, with a wavefront's loads of one block ahead of its products; two blocks
-// ahead 83 us.  Grouped, the workgroups of a block take its pieces of 16 rows in
-// steps of `step` rows.
+// ahead 2 us more.  Grouped, the workgroups of a block take its pieces of 16 rows
+// in steps of `step` rows.
 constexpr int kSplit = 8;
 template <int MT, int NT, bool GROUPED>
-__global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParams p, int ntiles, int step) {
+__global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParams p, int ntiles, uint32_t step) {
   __shared__ f32x4_t red[kSplit][MT * NT][kWave];
   const int tile = blockIdx.x % (p.S * ntiles);
   const int slice = tile / ntiles, n0 = (tile % ntiles) * 16 * NT;
   const int lane = lane_id(), w = wave_id(), a = lane & 15, g = lane >> 4;
-  int64_t first = int64_t(blockIdx.x / (p.S * ntiles)) * 16 * MT, start = 0, stop = 0;
+  const uint32_t piece = blockIdx.x / (p.S * ntiles);
+  const int64_t first = int64_t(piece) * 16 * MT;  // dense: the first row
   int64_t e = 0;
-  // grouped: the block's ids, one or two a lane, and which of them are a pair's
+  // grouped: the block's ids, one or two a lane, which of them are a pair's, and
+  // where in the block the piece begins
   int32_t id0 = -1, id1 = -1;
   uint64_t held0 = 0, held1 = 0;
-  // the first piece from `first` on, in this workgroup's steps, that has one
+  uint32_t at = 0;
+  const uint32_t block_m = p.block_m;
+  // goes to the first piece from `at` on, in this workgroup's steps, that has a pair
   auto seek = [&]() {
-    for (; first < stop; first += step) {
-      const int at = int(first - start);
-      if ((at < kWave ? held0 : held1) >> (at % kWave) & ((uint64_t(1) << 16 * MT) - 1)) return;
-    }
+    for (; at < block_m; at += step)
+      if ((at < kWave ? held0 : held1) >> (at % kWave) & ((uint64_t(1) << 16 * MT) - 1)) return true;
+    return false;
   };
   // row i of the piece
   auto row_at = [&](int i) {
-    if constexpr (GROUPED) {
-      const int at = int(first - start);
+    if constexpr (GROUPED)
       return row_of_pair(p, uint32_t(__shfl(at < kWave ? id0 : id1, at % kWave + i)));
-    } else {
+    else
       return row_of<false>(p, first, i);
-    }
   };
   if constexpr (GROUPED) {
-    const int q = blockIdx.x / (p.S * ntiles), block = q % p.blocks;
-    start = int64_t(block) * p.block_m;
-    first = start + q / p.blocks * (16 * MT);
-    stop = start + p.block_m;
-    // (what is behind the last block is read too, in one wait, and not used)
+    // A block's workgroups are neighbours, and what lies behind the last block
+    // comes last, when nothing waits for its place (8 experts of 512 x 1024, 96
+    // rows each: 9.5 us; a block's first pieces, then all second ones, 11.1).
+    const uint32_t parts = step / (16 * MT), block = piece / parts;
+    at = piece % parts * (16 * MT);
+    const int64_t start = int64_t(block) * block_m;
+    const int32_t* ids = p.sorted + start;
+    // (read behind the last block, too, in one wait, and not used)
     const int32_t used = p.ntpp[0];
-    if (lane < p.block_m) id0 = p.sorted[start + lane];
-    if (kWave + lane < p.block_m) id1 = p.sorted[start + kWave + lane];
+    if (uint32_t(lane) < block_m) id0 = ids[lane];
+    if (uint32_t(kWave + lane) < block_m) id1 = ids[kWave + lane];
     e = p.eids[block];
+    if (start >= used || e < 0 || e >= p.E) return;
     held0 = __ballot(uint32_t(id0) < uint32_t(p.numel));
     held1 = __ballot(uint32_t(id1) < uint32_t(p.numel));
-    if (start >= used || e < 0 || e >= p.E) return;
-    seek();
-    if (first >= stop) return;  // padding
+    if (!seek()) return;  // padding
   }
 
   const uint8_t* wbase = p.w + (e * p.S + slice) * p.Ns * int64_t(p.K);
@@ -196,9 +199,8 @@ __global__ void __launch_bounds__(kSplit * kWave) fp8_gemm_rows_kernel(GemmParam
       *reinterpret_cast<uint2*>(p.y + r.y_row * (int64_t(p.S) * p.Ns) + slice * p.Ns + n) = o;
     }
     if constexpr (!GROUPED) return;
-    first += step;
-    seek();
-    if (first >= stop) return;
+    at += step;
+    if (!seek()) return;
     __syncthreads();  // the sums have been read
   }
 }
