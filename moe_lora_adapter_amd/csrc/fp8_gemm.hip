@@ -381,8 +381,9 @@ struct TileList {
 // A stage's two operands are read from LDS by WN and WM wavefronts: at 128 x 64 a
 // wavefront (256 x 256) that is 24 KiB for 32 MFMAs of 32 cycles, which LDS
 // serves in half that time; 128 accumulators are what leaves registers for it.
-// 4096 x 4096 x 12288: 183 us, 2.25 PFLOP/s, the matrix cores 55 % busy at the
-// 1.97 GHz the load leaves.  Without the loads the same loop takes 141 us, the
+// 4096 x 4096 x 12288: 180 us once the card's clock has settled (some 200 calls;
+// 212 before), 2.29 PFLOP/s, the matrix cores 53 % busy at the 2.0 GHz of the run
+// that counted.  Without the loads the same loop takes 141 us, the
 // loads alone 89: what is between is stages whose loads take longer than their
 // MFMAs, with two of them filling the LDS.
 //
@@ -770,7 +771,7 @@ hipError_t tile_launch(GemmParams p, hipStream_t st) {
 // Pieces of an align block that start at once: as many as an expert has on
 // average, a block's workgroups take the others in turn.  Starting every piece
 // would leave most workgroups to find padding: 64 experts of 256 x 512, 8 rows
-// each in blocks of 64, 4.1 us and 8.5.
+// each in blocks of 64, 8.5 us, so 4.9; 8 of 2048 x 4096 29.3 and 17.2.
 template <int MT>
 int64_t parts_of(const GemmParams& p) {
   const int64_t each = p.numel / (int64_t(p.E) * 12) + 1;
@@ -851,10 +852,12 @@ hipError_t launch_fp8_gemm(GemmParams p, hipStream_t st) {
 // weights at 5.5 TB/s.  The rows kernel takes 3 us, and for each piece of 16 rows
 // those weights or 4 ns a workgroup; the tiles take 10 us, of which most is
 // finding them, and each expert's weights once, or, with few of them, the
-// latency of their K.  Measured, rows and tiles: 8 experts of 512 x 1024, 8 rows
-// each, 3.4 and 9.3, 96 rows 8.5 and 10.7; 8 of 2048 x 4096, 8 rows 14.5 and
-// 23.6, 48 rows 39 and 27; 128 of 2880 x 2880, 4 rows 181 and 192, 8 rows 199 and
-// 200, 16 rows 254 and 209.
+// latency of their K.  Measured with W from memory, rows and tiles: 8 experts of
+// 512 x 1024, 8 rows each, 4.5 and 12.1, 96 rows 9.6 and 13.6; 8 of 2048 x 4096,
+// 8 rows 17.2 and 31.8, 48 rows 40 and 36; 128 of 2880 x 2880, 4 rows 178 and 193,
+// 8 rows 197 and 201, 16 rows 260 and 210.  Routing that leaves most pairs to few
+// experts is not seen: the rows kernel then reads their weights once for every 16
+// rows, whatever the tiles would take.
 hipError_t launch_fp8_moe_gemm(GemmParams p, hipStream_t st) {
   const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
   const int64_t E = p.E, used = std::min<int64_t>(p.numel, E);
@@ -867,8 +870,9 @@ hipError_t launch_fp8_moe_gemm(GemmParams p, hipStream_t st) {
   if (by_rows <= by_tiles && rows_fit(rows_grid<1, 2, true>(p))) {
     // 64 columns a workgroup read X half as often as 32, which is worth it from a
     // few rows an expert on and with a workgroup for every CU (64 experts of 1024
-    // x 4096: 1 row each 36.3 us and 32.7, 8 rows 52.3 and 53.7; 128 of 2880 x
-    // 2880, 8 rows 199 and 215; 8 of 512 x 1024, 8 rows 4.0 and 3.4)
+    // x 4096: 1 row each 38.0 us and 35.6, 8 rows 56.0 and 53.4; 128 of 2880 x
+    // 2880, 4 rows 178 and 182, 8 rows 197 and 214; 8 of 512 x 1024, 8 rows 5.4
+    // and 4.5)
     if (p.numel >= 3 * E && used * p.S * ((p.Ns + 63) / 64) >= cus) return rows_of<1, 4, true>(p, st);
     return rows_of<1, 2, true>(p, st);
   }
