@@ -486,7 +486,8 @@ MOE_LORA_API int moe_lora_silu_mul_fp8(const uint16_t *y, int64_t P, int32_t I, 
  *          no input.
  * K a multiple of 16, Ns of 8; x, w and y 16-byte aligned.
  * MOE_LORA_ERR_UNSUPPORTED for K > 2^22, when a slice of w has 2^31 elements or
- * more, S*Ns does, or x_scales exceeds 2 GiB.  M == 0 does nothing.  Deterministic.
+ * more, S*Ns does, x_scales exceeds 2 GiB, or y has 2^31 tiles of 16 x 16 or more
+ * (a slice's last one counted whole).  M == 0 does nothing.  Deterministic.
  */
 MOE_LORA_API int moe_lora_fp8_gemm(const uint8_t *x, const float *x_scales, const uint8_t *w,
                    const float *w_scales, int64_t M, int32_t K, int32_t Ns, int32_t S,
@@ -511,8 +512,9 @@ MOE_LORA_API int moe_lora_fp8_gemm(const uint8_t *x, const float *x_scales, cons
  *          input.
  * Sizes and alignment as moe_lora_align and moe_lora_fp8_gemm; block_m is the
  * align outputs' and sets no tile (blocks of one expert are taken together);
- * MOE_LORA_ERR_UNSUPPORTED also when x exceeds 2 GiB.  M == 0 does nothing.
- * Deterministic.
+ * MOE_LORA_ERR_UNSUPPORTED also when x exceeds 2 GiB; the tiles of y are counted
+ * over the rows of all blocks that the align outputs have room for.  M == 0 does
+ * nothing.  Deterministic.
  */
 MOE_LORA_API int moe_lora_fp8_moe_gemm(const uint8_t *x, const float *x_scales,
                    int32_t x_per_pair, const uint8_t *w, const float *w_scales,
