@@ -14,7 +14,8 @@
  *
  * and, further down, the 8-bit base side they stand beside: rows of e4m3
  * values from an RMS norm or a gated activation, and the e4m3 product, dense
- * or over the align step's blocks.
+ * or over the align step's blocks; and the bf16 base side: routing, the bf16
+ * product with an epilogue, dense or over the align step's blocks, and combine.
  *
  * Conventions for every call below:
  *   - Pointers marked [device] are device (HBM) addresses; the caller owns
@@ -522,6 +523,146 @@ MOE_LORA_API int moe_lora_fp8_moe_gemm(const uint8_t *x, const float *x_scales,
                    const int32_t *num_tokens_post_padded, const float *topk_weights,
                    int32_t mul_routed_weight, int64_t M, int32_t topk, int32_t K, int32_t Ns,
                    int32_t S, int32_t E, int32_t block_m, uint16_t *y, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The bf16 base side of a layer: router -> (align) -> experts' products ->
+ * (adapters) -> combine, and the dense product beside them.  The pages' base
+ * fused-MoE path takes routed weights and experts from a top-k over the router's
+ * logits, and ends in the sum over a token's experts (prhub summary of vLLM PR
+ * #42290, the TritonExperts fragment).
+ * ------------------------------------------------------------------------ */
+
+/* Most picks a token and most experts of moe_lora_route. */
+#define MOE_LORA_ROUTE_MAX_TOPK 64
+#define MOE_LORA_ROUTE_MAX_EXPERTS 1024
+
+/* How moe_lora_route scores a logit. */
+enum moe_lora_scoring {
+    MOE_LORA_SCORING_SOFTMAX = 0, /* exp(x) / sum of exp(x) over the row */
+    MOE_LORA_SCORING_SIGMOID = 1  /* 1 / (1 + exp(-x))                   */
+};
+
+/*
+ * moe_lora_route -- the experts of every token, in the form moe_lora_align and
+ * the products take them.  For a row x of logits:
+ *     s[e]   = the score of x[e]
+ *     key[e] = s[e] + bias[e], or s[e] (group_top == 2, no bias), or x[e]
+ *     groups: experts g*(E/n_group) .. (g+1)*(E/n_group)-1; a group's score is
+ *             the sum of its group_top (1 or 2) largest keys; the topk_group
+ *             groups with the largest scores stay, ties to the lowest group
+ *     picks:  the topk largest keys of those groups in descending order, ties to
+ *             the lowest expert
+ *     topk_weights[m, k] = scale * s[pick] (/ the sum of s over the row's picks,
+ *             when renormalize)
+ * The bias moves which experts are picked and not their weights.  Scores decide
+ * as in fp64: what is picked does not hang on a rounding to fp32.  The weights
+ * are computed in fp32.
+ * An expert whose logit or bias is -infinity is masked: it is never picked.
+ * Where fewer than topk are left, the remaining places get id -1 and weight 0
+ * (moe_lora_align and every product pass over them; so does moe_lora_combine
+ * given the ids).  A group without an expert left is never kept before one that
+ * has some.  NaN (a logit, or a key of an expert that is not masked) is never
+ * picked, and makes all weights of its row NaN.  A logit of +infinity has all of
+ * a softmax, in equal parts where there are several.
+ * [device] logits: fp32 or bf16 [M, E] (logits_bf16); bias: fp32 [E] or NULL;
+ *          topk_ids: int32 [M, topk]; topk_weights: fp32 [M, topk]; outputs
+ *          overlap no input.
+ * logits aligned to their type, the others to 4 bytes.  MOE_LORA_ERR_INVALID when
+ * n_group does not divide E, topk_group is outside [1, n_group], group_top
+ * outside [1, 2] or above E / n_group, topk above topk_group * E / n_group, scale
+ * not finite, or a flag not 0 or 1.  With n_group == 1, group_top == 2 is
+ * refused, too.  MOE_LORA_ERR_UNSUPPORTED for E > MOE_LORA_ROUTE_MAX_EXPERTS, topk
+ * > MOE_LORA_ROUTE_MAX_TOPK, n_group > 64 or M * topk >= 2^31.  M == 0 does
+ * nothing.  Deterministic.
+ */
+MOE_LORA_API int moe_lora_route(const void *logits, int32_t logits_bf16, const float *bias,
+                   int64_t M, int32_t E, int32_t topk, int32_t scoring, int32_t n_group,
+                   int32_t topk_group, int32_t group_top, int32_t renormalize, float scale,
+                   int32_t *topk_ids, float *topk_weights, void *stream);
+
+/* What a product's epilogue applies. */
+enum moe_lora_activation {
+    MOE_LORA_ACT_NONE = 0,
+    MOE_LORA_ACT_SILU = 1,        /* z / (1 + exp(-z))                              */
+    MOE_LORA_ACT_GELU_TANH = 2,   /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))  */
+    /* gated, of z = [gate | up] (S = 2): one output of width Ns                    */
+    MOE_LORA_ACT_SILU_MUL = 3,    /* gate / (1 + exp(-gate)) * up                   */
+    MOE_LORA_ACT_SWIGLU_CLAMP = 4 /* a / (1 + exp(-1.702 a)) * (b + 1),
+                                     a = min(gate, 7), b = min(max(up, -7), 7)      */
+};
+
+/*
+ * moe_lora_gemm -- for every row m and column n < S*Ns:
+ *     z[m, n] = sum_k x[m, k] * w[n, k] + bias[n] + delta[m, n]
+ *     y[m, :] = activation(z[m, :]) + residual[m, :]
+ * Sums and epilogue are fp32, y is rounded once.  delta is what the adapters add
+ * before an activation (fused_moe_lora with add_inputs = 0, on a stream of its
+ * own or before this call); without an activation it is a second residual.  The
+ * sigmoid and its exponential are the hardware's: off by some (3 + |z|) 2^-23 of
+ * their value, and 0 where the exponential exceeds fp32 (z below -88).
+ * [device] x: bf16 [M, K]; w: bf16 [S, Ns, K]; bias: bf16 [S*Ns] or NULL; delta:
+ *          bf16 [M, S*Ns] or NULL; residual: bf16 [M, No] or NULL; y: bf16 or
+ *          (y_fp32) fp32 [M, No]; No = Ns with a gated activation, else S*Ns.  y
+ *          may be residual itself, and delta itself without a gated activation
+ *          (bf16 y); otherwise it overlaps no input.
+ * K and Ns multiples of 8; all pointers 16-byte aligned.  MOE_LORA_ERR_INVALID for
+ * a gated activation with S != 2.  MOE_LORA_ERR_UNSUPPORTED for K > 2^21, when w has
+ * 2^30 elements or more, or y has 2^31 tiles of 16 x 16 or more.  M == 0 does
+ * nothing.  Deterministic.
+ */
+MOE_LORA_API int moe_lora_gemm(const uint16_t *x, const uint16_t *w, const uint16_t *bias,
+                   const uint16_t *delta, const uint16_t *residual, int64_t M, int32_t K,
+                   int32_t Ns, int32_t S, int32_t activation, int32_t y_fp32, void *y,
+                   void *stream);
+
+/*
+ * moe_lora_moe_gemm -- the same product for the routed pairs: for every pair
+ * p = m*topk + k in the align outputs (of one slot: moe_lora_align with L = 1 and
+ * a zero mapping), with its block's expert e,
+ *     z[p, n] = w[p] * (sum_k x[row, k] * w[e, n, k] + bias[e, n]) + delta[p, n]
+ *     y[p, :] = activation(z[p, :]),
+ * row = p if x_per_pair else m, w[p] = topk_weights[p] if mul_routed_weight else
+ * 1.  Rows of pairs in no block are not touched.  Ids in sorted_token_ids outside
+ * [0, M*topk), wherever they stand, and blocks whose expert is outside [0, E) are
+ * passed over.
+ * [device] x: bf16 [M, K] or [M*topk, K]; w: bf16 [E, S, Ns, K]; bias: bf16
+ *          [E, S*Ns] or NULL; delta: bf16 [M, topk, S*Ns] or NULL (as
+ *          fused_moe_lora with add_inputs = 0 and the same mul_routed_weight
+ *          leaves it); sorted_token_ids [cap], expert_ids [cap / block_m],
+ *          num_tokens_post_padded [1]: moe_lora_align's for the same M, topk, E,
+ *          block_m; topk_weights: fp32 [M, topk], may be NULL when
+ *          mul_routed_weight == 0; y: bf16 [M, topk, No].  y may be delta itself
+ *          without a gated activation; otherwise it overlaps no input.
+ * Sizes, alignment and errors as moe_lora_align and moe_lora_gemm, the limit on
+ * w that of one expert; block_m is the align outputs' and sets no tile;
+ * MOE_LORA_ERR_UNSUPPORTED also when x has 2^30 elements or more; the tiles of y
+ * are counted over the rows of all blocks that the align outputs have room for.
+ * M == 0 does nothing.  Deterministic.
+ */
+MOE_LORA_API int moe_lora_moe_gemm(const uint16_t *x, int32_t x_per_pair, const uint16_t *w,
+                   const uint16_t *bias, const uint16_t *delta,
+                   const int32_t *sorted_token_ids, const int32_t *expert_ids,
+                   const int32_t *num_tokens_post_padded, const float *topk_weights,
+                   int32_t mul_routed_weight, int64_t M, int32_t topk, int32_t K, int32_t Ns,
+                   int32_t S, int32_t E, int32_t block_m, int32_t activation, uint16_t *y,
+                   void *stream);
+
+/*
+ * moe_lora_combine -- out[m, :] = bf16( sum_k w[m, k] * y[m, k, :] + residual[m, :] ):
+ * a token's expert outputs joined, in ascending k, in fp32, rounded once.  w is 1
+ * when topk_weights is NULL (the product has applied them).  With topk_ids, pairs
+ * whose id is outside [0, E) are left out, their rows of y not read (no product
+ * wrote them).
+ * [device] y: bf16 [M, topk, N]; topk_weights: fp32 [M, topk] or NULL; topk_ids:
+ *          int32 [M, topk] or NULL (then E is not used); residual: bf16 [M, N] or
+ *          NULL; out: bf16 [M, N], which may be residual itself and otherwise
+ *          overlaps no input.
+ * N a multiple of 8; y, residual and out 16-byte aligned.  MOE_LORA_ERR_UNSUPPORTED
+ * for M * topk >= 2^31 or M * N >= 2^34.  M == 0 does nothing.  Deterministic.
+ */
+MOE_LORA_API int moe_lora_combine(const uint16_t *y, const float *topk_weights,
+                   const int32_t *topk_ids, int32_t E, const uint16_t *residual, int64_t M,
+                   int32_t topk, int32_t N, uint16_t *out, void *stream);
 
 #ifdef __cplusplus
 }

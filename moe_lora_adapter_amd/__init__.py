@@ -15,6 +15,14 @@ The 8-bit base side of the same layer:
     moe_lora_fp8_moe_gemm(x8, w13, w13_scales, base_align, None, y, ...)
     h8 = moe_lora_silu_mul_fp8(y, h=h)
     moe_lora_fp8_moe_gemm(h8, w2, w2_scales, base_align, topk_weights, y2, ...)
+
+The bf16 base side, from the router's logits to the layer's output:
+
+    logits = moe_lora_gemm(x, gate, out_dtype=torch.float32)
+    ids, weights = moe_lora_route(logits, topk)
+    moe_lora_moe_gemm(x, w13, base_align, None, h, bias=..., delta=d13, activation="silu_mul", ...)
+    moe_lora_moe_gemm(h, w2, base_align, weights, y, mul_routed_weight=True, x_per_pair=True)
+    moe_lora_combine(y, residual=x)
 """
 
 from __future__ import annotations
@@ -72,6 +80,13 @@ SIGNATURES = {
     "moe_lora_fp8_gemm": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _P]),
     "moe_lora_fp8_moe_gemm": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P, _P, _I32, _I64,
                                              _I32, _I32, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_lora_route": (ctypes.c_int, [_P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                      ctypes.c_float, _P, _P, _P]),
+    "moe_lora_gemm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P,
+                                     _P]),
+    "moe_lora_moe_gemm": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I64, _I32,
+                                         _I32, _I32, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_lora_combine": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I64, _I32, _I32, _P, _P]),
 }
 
 NAIVE_MAX_PAIRS = 1024        # MOE_LORA_NAIVE_MAX_PAIRS
@@ -80,6 +95,11 @@ WITH_ALIGN_MAX_SLOTS = 64     # MOE_LORA_WITH_ALIGN_MAX_SLOTS
 TWO_KERNEL_MAX_RANK = 512     # MOE_LORA_TWO_KERNEL_MAX_RANK
 FP8_BLOCK = 128               # MOE_LORA_FP8_BLOCK
 RMS_NORM_MAX_WIDTH = 65536    # MOE_LORA_RMS_NORM_MAX_WIDTH
+ROUTE_MAX_TOPK = 64           # MOE_LORA_ROUTE_MAX_TOPK
+ROUTE_MAX_EXPERTS = 1024      # MOE_LORA_ROUTE_MAX_EXPERTS
+SCORINGS = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {None: 0, "silu": 1, "gelu_tanh": 2, "silu_mul": 3, "swiglu_clamp": 4}
+GATED = ("silu_mul", "swiglu_clamp")   # of gate and up: two slices in, one out
 
 
 class MoeLoraError(RuntimeError):
@@ -676,3 +696,189 @@ def moe_lora_fp8_moe_gemm(x: Fp8Rows, w, w_scales, align: AlignOutput, topk_weig
     if rc != OK:
         raise MoeLoraError(rc, "moe_lora_fp8_moe_gemm")
     return y
+
+
+def _align_ptrs(torch, align, M, topk, E, like, at):
+    """Checks one slot's align outputs on the device of `like`; their three addresses."""
+    i32, block_m = torch.int32, align.block_m
+    cap = align_capacity(M, topk, E, block_m)
+    ids, eids, ntpp = align.sorted_token_ids, align.expert_ids, align.num_tokens_post_padded
+    for t, name, want in ((ids, "sorted_token_ids", (1, cap)),
+                          (eids, "expert_ids", (1, cap // block_m)),
+                          (ntpp, "num_tokens_post_padded", (1,))):
+        if t.dtype is not i32 or t.shape != want or not t.is_contiguous() or t.get_device() != at:
+            _refuse(t, "align." + name, i32, like.device, want)
+    return ids.data_ptr(), eids.data_ptr(), ntpp.data_ptr()
+
+
+def _activation(name):
+    """Number of an activation, and whether it takes gate and up."""
+    try:
+        return ACTIVATIONS[name], name in GATED
+    except KeyError:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {name!r}") from None
+
+
+def _optional(t, name, dtype, shape, like, at):
+    """Address of a tensor that may be None, checked."""
+    if t is None:
+        return None
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != at):
+        _refuse(t, name, dtype, like.device, shape)
+    return t.data_ptr()
+
+
+def moe_lora_route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_group: int = 1,
+                   topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                   scale: float = 1.0, topk_ids=None, topk_weights=None, stream=None):
+    """Experts and weights of every row of logits [M, E] (fp32 or bf16): (topk_ids int32,
+    topk_weights fp32), both [M, topk], allocated when not given; -1 and 0 where no expert is
+    left; see moe_lora.h."""
+    import torch
+    bf16 = isinstance(logits, torch.Tensor) and logits.dtype is torch.bfloat16
+    if not bf16:
+        _check(logits, "logits", torch.float32, getattr(logits, "device", None))
+    elif not logits.is_contiguous():
+        _check(logits, "logits", torch.bfloat16, logits.device)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, E]")
+    if scoring not in SCORINGS:
+        raise ValueError(f"scoring must be one of {list(SCORINGS)}, got {scoring!r}")
+    M, E = logits.shape
+    at, want = logits.get_device(), (M, topk)
+    pb = _optional(bias, "bias", torch.float32, (E,), logits, at)
+    if topk_ids is None or topk_weights is None:
+        if topk < 1:
+            raise MoeLoraError(ERR_INVALID, "moe_lora_route")
+        with _taken_on(stream):
+            if topk_ids is None:
+                topk_ids = torch.empty(want, dtype=torch.int32, device=logits.device)
+            if topk_weights is None:
+                topk_weights = torch.empty(want, dtype=torch.float32, device=logits.device)
+    pi = _optional(topk_ids, "topk_ids", torch.int32, want, logits, at)
+    pw = _optional(topk_weights, "topk_weights", torch.float32, want, logits, at)
+    args = (logits.data_ptr(), 1 if bf16 else 0, pb, M, E, topk, SCORINGS[scoring], n_group,
+            topk_group, group_top, 1 if renormalize else 0, scale, pi, pw)
+    raw = _direct(torch, at, stream)
+    if raw is None:
+        _call("moe_lora_route", logits, stream, *args)
+        return topk_ids, topk_weights
+    rc = lib().moe_lora_route(*args, raw)
+    if rc != OK:
+        raise MoeLoraError(rc, "moe_lora_route")
+    return topk_ids, topk_weights
+
+
+def moe_lora_gemm(x, w, y=None, *, bias=None, delta=None, activation: str | None = None,
+                  residual=None, out_dtype=None, stream=None):
+    """activation(x w^T + bias + delta) + residual for w [S, Ns, K]; y [M, S*Ns] ([M, Ns] with a
+    gated activation) is bf16 or fp32, allocated as out_dtype (None: bf16) when not given; see
+    moe_lora.h."""
+    import torch
+    bf = torch.bfloat16
+    if not isinstance(w, torch.Tensor) or w.dtype is not bf or not w.is_contiguous():
+        _check(w, "w", bf, getattr(w, "device", None))
+    if w.dim() != 3 or x.dim() != 2:
+        raise ValueError("w must be [S, Ns, K] and x [M, K]")
+    S, Ns, K = w.shape
+    M, at, N = x.shape[0], w.get_device(), S * Ns
+    act, gated = _activation(activation)
+    No = Ns if gated else N
+    if x.dtype is not bf or x.shape != (M, K) or not x.is_contiguous() or x.get_device() != at:
+        _refuse(x, "x", bf, w.device, (M, K))
+    pb = _optional(bias, "bias", bf, (N,), w, at) if bias is not None else None
+    pd = _optional(delta, "delta", bf, (M, N), w, at) if delta is not None else None
+    pr = _optional(residual, "residual", bf, (M, No), w, at) if residual is not None else None
+    if y is None:
+        with _taken_on(stream):
+            y = torch.empty((M, No), dtype=bf if out_dtype is None else out_dtype, device=w.device)
+    elif out_dtype is not None and y.dtype is not out_dtype:
+        raise TypeError(f"y must be {out_dtype}, got {y.dtype}")
+    wide = y.dtype is torch.float32
+    if ((y.dtype is not bf and not wide) or y.shape != (M, No) or not y.is_contiguous()
+            or y.get_device() != at):
+        _refuse(y, "y", bf, w.device, (M, No))
+    args = (x.data_ptr(), w.data_ptr(), pb, pd, pr, M, K, Ns, S, act, 1 if wide else 0,
+            y.data_ptr())
+    raw = _direct(torch, at, stream)
+    if raw is None:
+        _call("moe_lora_gemm", w, stream, *args)
+        return y
+    rc = lib().moe_lora_gemm(*args, raw)
+    if rc != OK:
+        raise MoeLoraError(rc, "moe_lora_gemm")
+    return y
+
+
+def moe_lora_moe_gemm(x, w, align: AlignOutput, topk_weights, y, *, mul_routed_weight: bool,
+                      x_per_pair: bool = False, bias=None, delta=None,
+                      activation: str | None = None, stream=None):
+    """moe_lora_gemm with each routed pair's expert of w [E, S, Ns, K] and its bias [E, S*Ns], the
+    routed weight before delta [M, topk, S*Ns], into y [M, topk, S*Ns] ([M, topk, Ns] with a gated
+    activation); align is one slot's (L = 1); see moe_lora.h."""
+    import torch
+    bf = torch.bfloat16
+    if not isinstance(w, torch.Tensor) or w.dtype is not bf or not w.is_contiguous():
+        _check(w, "w", bf, getattr(w, "device", None))
+    if w.dim() != 4 or y.dim() != 3 or x.dim() != 2:
+        raise ValueError("w must be [E, S, Ns, K], y [M, topk, N] and x [rows, K]")
+    E, S, Ns, K = w.shape
+    at, N = w.get_device(), S * Ns
+    act, gated = _activation(activation)
+    M, topk, No = y.shape
+    if No != (Ns if gated else N):
+        raise ValueError(f"y's last dim must be {Ns if gated else N}, got {No}")
+    if y.dtype is not bf or not y.is_contiguous() or y.get_device() != at:
+        _check(y, "y", bf, w.device)
+    rows = M * topk if x_per_pair else M
+    if x.dtype is not bf or x.shape != (rows, K) or not x.is_contiguous() or x.get_device() != at:
+        _refuse(x, "x", bf, w.device, (rows, K))
+    pb = _optional(bias, "bias", bf, (E, N), w, at) if bias is not None else None
+    pd = _optional(delta, "delta", bf, (M, topk, N), w, at) if delta is not None else None
+    ptw = None
+    if topk_weights is not None:
+        ptw = _optional(topk_weights, "topk_weights", torch.float32, (M, topk), w, at)
+    pids, peids, pntpp = _align_ptrs(torch, align, M, topk, E, w, at)
+    args = (x.data_ptr(), 1 if x_per_pair else 0, w.data_ptr(), pb, pd, pids, peids, pntpp, ptw,
+            1 if mul_routed_weight else 0, M, topk, K, Ns, S, E, align.block_m, act, y.data_ptr())
+    raw = _direct(torch, at, stream)
+    if raw is None:
+        _call("moe_lora_moe_gemm", w, stream, *args)
+        return y
+    rc = lib().moe_lora_moe_gemm(*args, raw)
+    if rc != OK:
+        raise MoeLoraError(rc, "moe_lora_moe_gemm")
+    return y
+
+
+def moe_lora_combine(y, out=None, *, topk_weights=None, topk_ids=None, E: int | None = None,
+                     residual=None, stream=None):
+    """sum over k of y [M, topk, N] (times topk_weights) + residual, into out [M, N] (allocated when
+    not given); with topk_ids, pairs whose id is outside [0, E) are left out; see moe_lora.h."""
+    import torch
+    bf = torch.bfloat16
+    if not isinstance(y, torch.Tensor) or y.dtype is not bf or not y.is_contiguous():
+        _check(y, "y", bf, getattr(y, "device", None))
+    if y.dim() != 3:
+        raise ValueError("y must be [M, topk, N]")
+    if topk_ids is not None and E is None:
+        raise ValueError("topk_ids needs E, the number of experts here")
+    M, topk, N = y.shape
+    at = y.get_device()
+    pw = _optional(topk_weights, "topk_weights", torch.float32, (M, topk), y, at)
+    pi = _optional(topk_ids, "topk_ids", torch.int32, (M, topk), y, at)
+    pr = _optional(residual, "residual", bf, (M, N), y, at)
+    if out is None:
+        with _taken_on(stream):
+            out = torch.empty((M, N), dtype=bf, device=y.device)
+    po = _optional(out, "out", bf, (M, N), y, at)
+    args = (y.data_ptr(), pw, pi, E or 0, pr, M, topk, N, po)
+    raw = _direct(torch, at, stream)
+    if raw is None:
+        _call("moe_lora_combine", y, stream, *args)
+        return out
+    rc = lib().moe_lora_combine(*args, raw)
+    if rc != OK:
+        raise MoeLoraError(rc, "moe_lora_combine")
+    return out
