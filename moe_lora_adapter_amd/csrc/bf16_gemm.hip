@@ -11,6 +11,7 @@
 // is the epilogue; Y is rounded once.
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "base.h"
 #include "common.h"
@@ -23,6 +24,19 @@ namespace {
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+
+// f(0), f(1), ..., f(N - 1) with constants as arguments: arrays that only constants
+// index are registers, however much code there is (a loop that is unrolled late
+// leaves them in memory).
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+  each_of(static_cast<F&&>(f), std::make_integer_sequence<int, N>{});
+}
 
 constexpr int kStageK = 64;  // of K a stage: 128 bytes
 
@@ -39,31 +53,35 @@ __device__ __forceinline__ f32x4_t widen(const uint2& v) {
 // |v| 2^-23 of its value, and its reciprocal; 0 from v = -88.7 down
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
 
-__device__ __forceinline__ f32x4_t activate(f32x4_t v, int act) {
-  if (act == kActSilu) {
+__device__ __forceinline__ f32x4_t silu(f32x4_t v) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] *= sigmoid(v[j]);
-  } else if (act == kActGeluTanh) {
-    // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u))
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] *= sigmoid(1.5957691216057308f * (v[j] + 0.044715f * v[j] * v[j] * v[j]));
-  }
+  for (int j = 0; j < 4; ++j) v[j] *= sigmoid(v[j]);
   return v;
 }
-__device__ __forceinline__ f32x4_t gate_up(f32x4_t g, f32x4_t u, int act) {
-  if (act == kActSiluMul) {
+// (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u))
+__device__ __forceinline__ f32x4_t gelu_tanh(f32x4_t v) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) g[j] = g[j] * sigmoid(g[j]) * u[j];
-  } else {
-    // the clamps keep NaN
+  for (int j = 0; j < 4; ++j) v[j] *= sigmoid(1.5957691216057308f * (v[j] + 0.044715f * v[j] * v[j] * v[j]));
+  return v;
+}
+// (the clamps keep NaN)
+__device__ __forceinline__ f32x4_t swiglu_clamp(f32x4_t g, f32x4_t u) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = g[j] > 7.0f ? 7.0f : g[j];
-      const float b = u[j] > 7.0f ? 7.0f : (u[j] < -7.0f ? -7.0f : u[j]);
-      g[j] = a * sigmoid(1.702f * a) * (b + 1.0f);
-    }
+  for (int j = 0; j < 4; ++j) {
+    const float a = g[j] > 7.0f ? 7.0f : g[j];
+    const float b = u[j] > 7.0f ? 7.0f : (u[j] < -7.0f ? -7.0f : u[j]);
+    g[j] = a * sigmoid(1.702f * a) * (b + 1.0f);
   }
   return g;
+}
+__device__ __forceinline__ f32x4_t activate(f32x4_t v, f32x4_t u, int act) {
+  switch (act) {
+    case kActSilu: return silu(v);
+    case kActGeluTanh: return gelu_tanh(v);
+    case kActSiluMul: return silu(v) * u;
+    case kActSwigluClamp: return swiglu_clamp(v, u);
+    default: return v;
+  }
 }
 
 // Four columns of a row of Y from the sums of them (and of the up columns).
@@ -83,7 +101,7 @@ __device__ __forceinline__ f32x4_t finish(const ProductParams& p, f32x4_t v, f32
     v += four(d);
     if (p.gated) u += four(d + up);
   }
-  v = p.gated ? gate_up(v, u, p.act) : activate(v, p.act);
+  v = activate(v, u, p.act);
   if (p.residual) v += four(p.residual + y * p.No + col);
   return v;
 }
@@ -94,6 +112,109 @@ __device__ __forceinline__ void store(const ProductParams& p, f32x4_t v, int64_t
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) =
         make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// The same for a wavefront's part of a tile, one step of the epilogue after the
+// other over all of it.  at(i) is the row of Y or -1, wt(i) its weight, `col` the
+// first column of this lane; acc[i][f] and acc[i][f + 1] are columns col + 16 f ..
+// + 7, or, gated, gate and up of columns col + 8 f .. + 3.  Operands are read at a
+// place that is there, whether or not the row and the column are, and only stores
+// are left out; the loads of kAtOnce rows are in flight together.
+template <int FM, int FN, bool GROUPED, class At, class Weight>
+__device__ __forceinline__ void finish_tile(const ProductParams& p, f32x4_t (&acc)[FM][FN], At at, Weight wt,
+                                            const uint16_t* bias, int col) {
+  constexpr int kAtOnce = FM < 4 ? FM : FN > 2 ? 2 : 4;
+  static_assert(FM % kAtOnce == 0, "rows");
+  const bool gated = p.gated;
+  const int wide = gated ? 8 : 16;
+  // a pair of sums' eight values of an operand whose rows have gate and up
+  auto eight = [&](const uint16_t* from, int f) {
+    const uint16_t* a = from + min(col + wide * f, p.No - (gated ? 4 : 8));
+    if (!gated) return *reinterpret_cast<const uint4*>(a);
+    const uint2 g = *reinterpret_cast<const uint2*>(a), u = *reinterpret_cast<const uint2*>(a + p.No);
+    return make_uint4(g.x, g.y, u.x, u.y);
+  };
+  auto four = [&](const uint16_t* from, int f) {  // of one whose rows have not
+    const uint16_t* a = from + min(col + wide * f, p.No - (gated ? 4 : 8));
+    if (!gated) return *reinterpret_cast<const uint4*>(a);
+    const uint2 g = *reinterpret_cast<const uint2*>(a);
+    return make_uint4(g.x, g.y, 0, 0);
+  };
+  if (bias) {
+    each<FN / 2>([&](auto h) {
+      constexpr int f = 2 * h;
+      const uint4 b = eight(bias, f);
+      const f32x4_t lo = widen(make_uint2(b.x, b.y)), hi = widen(make_uint2(b.z, b.w));
+      each<FM>([&](auto i) { acc[i][f] += lo, acc[i][f + 1] += hi; });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+  if constexpr (GROUPED) {
+    if (p.wt)
+      each<FM>([&](auto i) {
+        const float w = wt(i);
+        each<FN>([&](auto f) { acc[i][f] *= w; });
+      });
+  }
+  // adds an operand, read by `get`
+  auto add = [&](const uint16_t* from, int width, auto get) {
+    asm volatile("" : "+v"(col));  // addresses are not to be kept: the registers are needed
+    each<FM / kAtOnce>([&](auto part) {
+      constexpr int i0 = part * kAtOnce;
+      uint4 d[kAtOnce][FN / 2];
+      each<kAtOnce>([&](auto i) {
+        const uint16_t* line = from + max(at(i0 + i), int64_t(0)) * width;
+        each<FN / 2>([&](auto h) { d[i][h] = get(line, 2 * h); });
+      });
+      each<kAtOnce>([&](auto i) {
+        each<FN / 2>([&](auto h) {
+          acc[i0 + i][2 * h] += widen(make_uint2(d[i][h].x, d[i][h].y));
+          acc[i0 + i][2 * h + 1] += widen(make_uint2(d[i][h].z, d[i][h].w));
+        });
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  if (p.delta) add(p.delta, p.N, eight);
+  // without an activation the residual is a second delta
+  const bool late = !GROUPED && p.residual && p.act != kActNone;
+  if constexpr (!GROUPED) {
+    if (p.residual && !late) add(p.residual, p.No, four);
+  }
+  asm volatile("" : "+v"(col));
+  each<FM>([&](auto i) {
+    __builtin_amdgcn_sched_barrier(0);
+    const int64_t m = at(i);
+    each<FN / 2>([&](auto h) {
+      const int n = col + wide * 2 * h;
+      if (m < 0 || n >= p.No) return;
+      f32x4_t v = acc[i][2 * h], u = acc[i][2 * h + 1];
+      const int64_t to = m * p.No + n;
+      if (gated) {
+        v = activate(v, u, p.act);
+      } else if (p.act != kActNone) {
+        v = activate(v, u, p.act);
+        u = activate(u, u, p.act);
+      }
+      if (late) {
+        const uint4 r = four(p.residual + m * p.No, 2 * h);
+        v += widen(make_uint2(r.x, r.y));
+        u += widen(make_uint2(r.z, r.w));
+      }
+      if (p.out32) {
+        float* y = static_cast<float*>(p.y) + to;
+        *reinterpret_cast<f32x4_t*>(y) = v;
+        if (!gated) *reinterpret_cast<f32x4_t*>(y + 4) = u;
+      } else {
+        uint16_t* y = static_cast<uint16_t*>(p.y) + to;
+        const uint2 lo = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        if (gated)
+          *reinterpret_cast<uint2*>(y) = lo;
+        else
+          *reinterpret_cast<uint4*>(y) = make_uint4(lo.x, lo.y, pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]));
+      }
+    });
+  });
 }
 
 // ---------------------------------------------------------------- few rows
@@ -282,12 +403,13 @@ struct Tile {
 };
 
 template <int WM, int WN, int FM, int FN, int NS, bool GROUPED, int KG>
-__global__ void __launch_bounds__(WM * WN * KG * kWave, 2) gemm_tile_kernel(ProductParams p, int ntiles) {
+__global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
+    gemm_tile_kernel(ProductParams p, int ntiles) {
   using T = Tile<WM, WN, FM, FN, NS, KG>;
   constexpr int BM = T::BM, BN = T::BN, XI = T::XI, WI = T::WI, kLoads = T::kLoads;
-  // whether the columns' loads run ahead of the rows' (below)
-  constexpr bool kEarly = FM > 2;
-  static_assert(KG == 1 || (!GROUPED && !kEarly), "a stage of several K blocks");
+  constexpr bool kPhases = FM > 2;  // (below)
+  static_assert(KG == 1 || (!GROUPED && !kPhases), "a stage of several K blocks");
+  static_assert(!kPhases || NS == 2, "phases");
   constexpr int kX = T::kX, kW = T::kW, kStage = T::kStage;
   const int stages = (p.KB + KG - 1) / KG;  // of a tile
   __shared__ __align__(1024) uint8_t lds[T::lds_bytes(GROUPED)];
@@ -417,13 +539,13 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2) gemm_tile_kernel(Prod
   const int ko = kg * T::kBlock;  // this wavefront's K block of a stage
   const int xo = ko + kX + xrow * 128 + 16 * (g ^ (a & 7));
   const int wo = ko + kW + wrow * 128 + 16 * (g ^ (a & 7));
-  constexpr int kWait = (NS - 2) * kLoads + (kEarly ? WI : 0);  // younger loads at a stage's barrier
+  constexpr int kWait = (NS - 2) * kLoads;  // younger loads at a stage's barrier
 
   set_tile();
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
 #pragma unroll
-    for (int l = 0; l < kLoads; ++l) load(l);
+    for (int l = 0; l < kLoads; ++l) load(kPhases ? (l + XI) % kLoads : l);
     loaded();
     if (lkb == stages) next_loads();
   }
@@ -447,15 +569,18 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2) gemm_tile_kernel(Prod
     }
     if (none) {
       for (int kb = 0; kb < stages; ++kb) {
-        if constexpr (kEarly) {
-          asm volatile("s_barrier" ::: "memory");
+        if constexpr (kPhases) {
+          stage_barrier<XI>();
 #pragma unroll
           for (int l = XI; l < XI + WI; ++l) load(l);
-        }
-        stage_barrier<kWait>();
+          stage_barrier<WI>();
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l)
-          if (!kEarly || l < XI) load(l);
+          for (int l = 0; l < XI; ++l) load(l);
+        } else {
+          stage_barrier<kWait>();
+#pragma unroll
+          for (int l = 0; l < kLoads; ++l) load(l);
+        }
         loaded();
         stage = stage + 1 == NS ? 0 : stage + 1;
         if (lkb == stages) next_loads();
@@ -464,73 +589,116 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2) gemm_tile_kernel(Prod
       continue;
     }
 
-    // A stage is FM steps of 2 FN MFMAs: a step reads the next one's rows.  The
-    // stage's barrier stands before the last step, once every wavefront has its
-    // last rows of the stage in registers; behind it the stage's buffer is
-    // refilled, and each column operand is replaced by the next stage's after its
-    // last use.  With more than two steps a second barrier, behind the first step,
-    // says that every wavefront has the stage's columns in registers, and their
-    // buffer is refilled from there on.  The scheduling barriers keep the compiler
-    // from undoing this order.
     f32x4_t acc[FM][FN];
-    uint4 wf[2][FN], xf[2][2];
-    auto columns = [&](const uint8_t* st, int h, int f) {
-      const int o = 4096 * (f >> 1) + 512 * (f & 1);
-      wf[h][f] = *reinterpret_cast<const uint4*>(st + (h ? wo ^ 64 : wo) + o);
-    };
-    auto rows = [&](const uint8_t* st, int i) {
-      xf[i & 1][0] = *reinterpret_cast<const uint4*>(st + xo + 2048 * i);
-      xf[i & 1][1] = *reinterpret_cast<const uint4*>(st + (xo ^ 64) + 2048 * i);
-    };
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      columns(lds + stage * kStage, 0, f);
-      columns(lds + stage * kStage, 1, f);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) acc[i][f] = f32x4_t{0, 0, 0, 0};
-    }
-    rows(lds + stage * kStage, 0);
-    for (int kb = 0; kb < stages;) {
-      // the stages until the loads change their tile
-      const int n = std::min(stages - kb, stages - lkb);
-      for (int r = 0; r < n; ++r) {
-        const uint8_t* st = lds + stage * kStage;
-        stage = stage + 1 == NS ? 0 : stage + 1;
-        const uint8_t* nx = lds + stage * kStage;
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          if (kEarly && i == 1) asm volatile("s_barrier" ::: "memory");
-          if (i < FM - 1) {
-            rows(st, i + 1);
-          } else {
-            stage_barrier<kWait>();
-            rows(nx, 0);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-              const int at = h * FN + f;
-              acc[i][f] = mfma_bf16(wf[h][f], xf[i & 1][h], acc[i][f]);
-              if (i == FM - 1) {
-                columns(nx, h, f);
-#pragma unroll
-                for (int l = kLoads * at / (2 * FN); l < kLoads * (at + 1) / (2 * FN); ++l)
-                  if (!kEarly || l < XI) load(l);
-              }
-              if (kEarly && i >= 1 && i < FM - 1) {
-                constexpr int kSlots = kEarly ? (FM - 2) * 2 * FN : 1;
-                const int slot = (i - 1) * 2 * FN + at;
-#pragma unroll
-                for (int l = WI * slot / kSlots; l < WI * (slot + 1) / kSlots; ++l) load(XI + l);
+    each<FM * FN>([&](auto j) { acc[j / FN][j % FN] = f32x4_t{0, 0, 0, 0}; });
+    // The scheduling barriers keep the compiler from undoing the order below.
+    if constexpr (kPhases) {
+      // A stage is two phases of 32 of K, each FM steps of FN MFMAs.  The rows of a
+      // step are read kAhead steps before it, the other phase's columns during this
+      // one.  At the stage's middle every wavefront has all its columns in
+      // registers: the columns' buffer is refilled from there on, and the next
+      // stage's have to be there.  kAhead steps before its end the same holds for
+      // the rows.  So LDS reads and loads are spread evenly over the MFMAs, and a
+      // load has a whole stage to arrive.  4096 x 4096 x 12288: 289 us, 301 with one
+      // barrier a stage and the columns' reads behind it; 1 step ahead 295; four
+      // wavefronts of 128 x 128 each 303.
+      constexpr int kAhead = 2, kHeld = 4, kSteps = 2 * FM;
+      uint4 wf[2][FN], xf[kHeld];
+      auto columns = [&](const uint8_t* st, auto h, auto f) {
+        constexpr int o = 4096 * (f >> 1) + 512 * (f & 1);
+        wf[h][f] = *reinterpret_cast<const uint4*>(st + (h ? wo ^ 64 : wo) + o);
+      };
+      auto rows = [&](const uint8_t* st, auto s) {  // of step s of a stage
+        xf[s % kHeld] = *reinterpret_cast<const uint4*>(st + (s >= FM ? xo ^ 64 : xo) + 2048 * (s % FM));
+      };
+      each<FN>([&](auto f) { columns(lds + stage * kStage, std::integral_constant<int, 0>{}, f); });
+      each<kAhead>([&](auto s) { rows(lds + stage * kStage, s); });
+      for (int kb = 0; kb < stages;) {
+        // the stages until the loads change their tile
+        const int n = std::min(stages - kb, stages - lkb);
+        for (int r = 0; r < n; ++r) {
+          const uint8_t* st = lds + stage * kStage;
+          stage = stage + 1 == NS ? 0 : stage + 1;
+          const uint8_t* nx = lds + stage * kStage;
+          each<kSteps>([&](auto step) {
+            constexpr int s = step, h = s / FM, i = s % FM, ahead = s + kAhead;
+            if constexpr (s == FM) stage_barrier<XI>();
+            if constexpr (ahead == kSteps) stage_barrier<WI>();
+            rows(ahead < kSteps ? st : nx, std::integral_constant<int, ahead % kSteps>{});
+            each<FN>([&](auto f) {
+              acc[i][f] = mfma_bf16(wf[h][f], xf[s % kHeld], acc[i][f]);
+              // reads and loads, each behind an MFMA of its own
+              constexpr int slot = i * FN + f, kRead = (FM - kAhead) * FN;
+              each<FN>([&](auto c) {
+                if constexpr (slot == kRead * c / FN) columns(h ? nx : st, std::integral_constant<int, 1 - h>{}, c);
+              });
+              if constexpr (h == 1) {
+                each<WI>([&](auto l) {
+                  if constexpr (slot == 1 + (kRead - 1) * l / WI) load(XI + l);
+                });
+                each<XI>([&](auto l) {
+                  if constexpr (slot == kRead + kAhead * FN * l / XI) load(l);
+                });
               }
               __builtin_amdgcn_sched_barrier(0);
-            }
+            });
+          });
+          loaded();
         }
-        loaded();
+        kb += n;
+        if (lkb == stages) next_loads();
       }
-      kb += n;
-      if (lkb == stages) next_loads();
+    } else {
+      // A stage is FM steps of 2 FN MFMAs: a step reads the next one's rows.  The
+      // stage's barrier stands before the last step, once every wavefront has its
+      // last rows of the stage in registers; behind it the stage's buffer is
+      // refilled, and each column operand is replaced by the next stage's after its
+      // last use.
+      uint4 wf[2][FN], xf[2][2];
+      auto columns = [&](const uint8_t* st, auto h, auto f) {
+        constexpr int o = 4096 * (f >> 1) + 512 * (f & 1);
+        wf[h][f] = *reinterpret_cast<const uint4*>(st + (h ? wo ^ 64 : wo) + o);
+      };
+      auto rows = [&](const uint8_t* st, auto i) {
+        xf[i & 1][0] = *reinterpret_cast<const uint4*>(st + xo + 2048 * i);
+        xf[i & 1][1] = *reinterpret_cast<const uint4*>(st + (xo ^ 64) + 2048 * i);
+      };
+      constexpr std::integral_constant<int, 0> first;
+      each<2 * FN>([&](auto j) {
+        columns(lds + stage * kStage, std::integral_constant<int, j / FN>{}, std::integral_constant<int, j % FN>{});
+      });
+      rows(lds + stage * kStage, first);
+      for (int kb = 0; kb < stages;) {
+        const int n = std::min(stages - kb, stages - lkb);
+        for (int r = 0; r < n; ++r) {
+          const uint8_t* st = lds + stage * kStage;
+          stage = stage + 1 == NS ? 0 : stage + 1;
+          const uint8_t* nx = lds + stage * kStage;
+          each<FM>([&](auto i) {
+            constexpr bool last = i == FM - 1;
+            if constexpr (last) {
+              stage_barrier<kWait>();
+              rows(nx, first);
+            } else {
+              rows(st, std::integral_constant<int, i + 1>{});
+            }
+            each<2 * FN>([&](auto j) {
+              constexpr int h = j / FN, f = j % FN;
+              acc[i][f] = mfma_bf16(wf[h][f], xf[i & 1][h], acc[i][f]);
+              if constexpr (last) {
+                columns(nx, std::integral_constant<int, h>{}, std::integral_constant<int, f>{});
+                each<kLoads>([&](auto l) {
+                  if constexpr (l >= kLoads * j / (2 * FN) && l < kLoads * (j + 1) / (2 * FN)) load(l);
+                });
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            });
+          });
+          loaded();
+        }
+        kb += n;
+        if (lkb == stages) next_loads();
+      }
     }
 
     if constexpr (KG > 1) {
@@ -553,31 +721,16 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2) gemm_tile_kernel(Prod
     if constexpr (GROUPED) {
       if (bias) bias += int64_t(p.eids[p.block0 + list->block(row)]) * p.N;
     }
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      int64_t y;
-      float wt = 1.0f;
-      if constexpr (GROUPED) {
-        const int2 pr = pairs[ring * BM + xrow + 16 * i];
-        y = pr.x;
-        wt = __int_as_float(pr.y);
-      } else {
-        y = int64_t(row) * BM + xrow + 16 * i;
-        if (y >= p.M) y = -1;
-      }
-      if (y < 0) continue;
-#pragma unroll
-      for (int f = 0; f < FN; f += 2) {
-        const int col = gated ? n0 + 8 * f + 4 * g : n0 + 16 * f + 8 * g;
-        if (col >= p.No) continue;
-        if (gated) {
-          store(p, finish(p, acc[i][f], acc[i][f + 1], bias, y, col, wt), y, col);
-        } else {
-          store(p, finish(p, acc[i][f], acc[i][f], bias, y, col, wt), y, col);
-          store(p, finish(p, acc[i][f + 1], acc[i][f + 1], bias, y, col + 4, wt), y, col + 4);
-        }
-      }
-    }
+    const int2* own = pairs + ring * BM + xrow;
+    auto at = [&](int i) -> int64_t {
+      if constexpr (GROUPED) return own[16 * i].x;
+      int r = xrow + 16 * i;
+      asm volatile("" : "+v"(r));  // not to be kept: the registers are needed
+      const int64_t y = int64_t(row) * BM + r;
+      return y < p.M ? y : -1;
+    };
+    auto wt = [&](int i) { return __int_as_float(own[16 * i].y); };
+    finish_tile<FM, FN, GROUPED>(p, acc, at, wt, bias, gated ? n0 + 4 * g : n0 + 8 * g);
   }
   // no load into LDS outlives its workgroup
   __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
