@@ -20,6 +20,9 @@ struct RouteParams {
   int32_t n_group, topk_group, group_top;
   int32_t size;        // experts of a group
   uint32_t inv_size;   // e / size = e * inv_size >> 20, e < 1024
+  int32_t group_shift; // a group is the experts of 2^group_shift lanes; -1: not whole lanes
+  int32_t vectors;     // a lane's logits may be loaded together
+  int32_t slot_shift, batch; // a row's picks take 2^slot_shift lanes; rows a wavefront takes at once
   int32_t logits_bf16, sigmoid, renorm;
   float scale;
 };

@@ -5,10 +5,10 @@
 //   the topk largest keys of those, ties to the lowest index
 //   w   = scale * s[pick] (/ the sum of s over the picks)
 //
-// One wavefront a row; lane i holds the experts i, i + 64, ..., each lane's
-// sorted, so that a pick is one maximum over the lanes' first keys and one lane's
-// step to its next.  Bound by those steps (some 20 instructions a pick) and by the
-// loads of x.
+// One wavefront a row, V consecutive experts a lane, each lane's sorted, so that a
+// pick is one maximum over the lanes' first keys and one lane's step to its next,
+// and ties fall to the lowest lane.  Bound by those instructions (some 25 a pick,
+// 10 a score).
 //
 // Which of two nearly equal scores is larger must not hang on a rounding: keys
 // are computed in fp32, and a row where two keys that decide something are closer
@@ -25,11 +25,39 @@ namespace {
 
 constexpr int kWaves = 4;  // of a workgroup, a row each
 
+// ---------------------------------------------------------------- keys
+// fp32 keys are compared as unsigned integers in the same order, so that a step of
+// a maximum over lanes is one instruction; fp64 ones as they are.
+constexpr float kMasked = -__builtin_huge_valf();
+
+template <typename T>
+constexpr T none();  // below every key: masked, or picked already
+template <>
+constexpr uint32_t none<uint32_t>() { return 0; }
+template <>
+constexpr double none<double>() { return -__builtin_huge_val(); }
+
+// -infinity and NaN become none.
+template <typename T, typename F>
+__device__ __forceinline__ T key_of(F v) {
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t u = __float_as_uint(v);
+    return v > kMasked ? u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u) : none<T>();
+  } else {
+    return v > F(kMasked) ? v : none<T>();
+  }
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return k == none<uint32_t>() ? kMasked : __uint_as_float(k ^ (~uint32_t(int32_t(k) >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ double value_of(double k) { return k; }
+
+// ---------------------------------------------------------------- across lanes
 // Partner's value in a butterfly step, 32 or 64 bits.
 template <typename T>
 __device__ __forceinline__ T partner(T v, int o) {
   if constexpr (sizeof(T) == 4) {
-    return butterfly_partner(v, o);
+    return __builtin_bit_cast(T, butterfly_partner(__builtin_bit_cast(float, v), o));
   } else {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = __float_as_uint(butterfly_partner(__uint_as_float(uint32_t(u)), o));
@@ -37,21 +65,7 @@ __device__ __forceinline__ T partner(T v, int o) {
     return __builtin_bit_cast(T, uint64_t(hi) << 32 | lo);
   }
 }
-template <typename T>
-__device__ __forceinline__ T wave_max(T v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const T u = partner(v, o);
-    v = u > v ? u : v;
-  }
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += partner(v, o);
-  return v;
-}
+// `v` of lane `src` as a scalar.
 template <typename T>
 __device__ __forceinline__ T from_lane(T v, int src) {
   if constexpr (sizeof(T) == 4) {
@@ -63,92 +77,152 @@ __device__ __forceinline__ T from_lane(T v, int src) {
     return __builtin_bit_cast(T, uint64_t(hi) << 32 | lo);
   }
 }
+// The largest of the wavefront, a scalar.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ uint32_t max_step(uint32_t v) {
+  return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xf, false)));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max_step<0x111>(v);       // row_shr:1
+  v = max_step<0x112>(v);       // row_shr:2
+  v = max_step<0x114>(v);       // row_shr:4
+  v = max_step<0x118>(v);       // row_shr:8
+  v = max_step<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  v = max_step<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+  return from_lane(v, kWave - 1);
+}
+__device__ __forceinline__ double wave_max(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const double u = partner(v, o);
+    v = u > v ? u : v;
+  }
+  return from_lane(v, 0);
+}
+// Sum over the first `n` lanes (a power of two), in each of them.
+template <typename T>
+__device__ __forceinline__ T sum_over(T v, int n) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1)
+    if (o < n) v += partner(v, o);
+  return v;
+}
 
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ float exp_of(float v) { return __expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ float over_one(float v) { return __builtin_amdgcn_rcpf(v); }
 
 // exp(x - m), also where both are the same infinity
 template <typename T>
 __device__ __forceinline__ T exp_from(T x, T m) {
   return x == m ? T(1) : exp_of(x - m);
 }
+__device__ __forceinline__ float exact_exp_from(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
-template <typename T>
-constexpr T kNone = -T(__builtin_huge_val());  // masked, or picked already
-
-// Whether fp32 leaves open which of two keys a >= b is larger.  A score is off by
-// less than 2^-19: by the exponential (its argument's rounding |d| 2^-24 exp(d) and
-// its own, below 2^-22 of values up to 1), the sum (22 additions at most) and the
-// quotient; the bias adds a rounding of the key, a group's sum another.
-__device__ __forceinline__ bool open_between(float a, float b) {
-  return b > kNone<float> && !(a - b > 0x1p-17f + 0x1p-21f * fmaxf(fabsf(a), fabsf(b)));
+// Whether fp32 leaves open which of two keys, or groups' sums of two, a >= b is
+// larger.  A sigmoid is off by less than 2^-22: s (1 - s) times the exponential's
+// error (1.5 |x| 2^-24 for its argument, 2^-23 its own; |x| s (1 - s) < 1/4), the
+// addition's 2^-24 and the reciprocal's 2^-23.  A softmax's share is off by less than
+// 2^-18: up to 21 additions and the exponentials' errors (|d| < 8 on average) in the
+// sum.  The bias and a group's sum add roundings of the key.
+__device__ __forceinline__ bool open_between(float a, float b, int sigmoid) {
+  return b > kMasked && !(a - b > (sigmoid ? 0x1p-20f : 0x1p-16f) + 0x1p-21f * fmaxf(fabsf(a), fabsf(b)));
 }
-__device__ __forceinline__ bool open_between(double, double) { return false; }
+__device__ __forceinline__ bool open_between(double, double, int) { return false; }
 
-struct Picks {
-  int id;       // lane r: the r-th pick, or -1
-  bool open;    // (fp32) some decision is open
-};
+// ---------------------------------------------------------------- picking
+// Groups' ranks from their scores, the same in all `lanes` lanes of a group.
+// Returns whether fp32 leaves the cut open.
+template <typename F>
+__device__ __forceinline__ bool rank_groups(const RouteParams& p, F score, int group, int lanes, int* rank) {
+  int r = 0;
+  for (int g = 0; g < p.n_group; ++g) {
+    const F v = from_lane(score, g * lanes);
+    r += v > score || (v == score && g < group);
+  }
+  *rank = r;
+  if (p.topk_group == p.n_group) return false;
+  const uint64_t in = __ballot(group < p.n_group && r == p.topk_group - 1);
+  const uint64_t next = __ballot(group < p.n_group && r == p.topk_group);
+  return open_between(from_lane(score, __builtin_ctzll(in)), from_lane(score, __builtin_ctzll(next)), p.sigmoid);
+}
 
-// Picks by `key` (key[j] is expert 64 j + lane's; kNone: masked).  With CHECKED
-// fp32 keys, ends where a decision is open.
-template <typename T, int V, bool CHECKED>
-__device__ __forceinline__ Picks pick(const RouteParams& p, T (&key)[V], T* lds) {
-  const int lane = lane_id();
-  constexpr bool kCheck = CHECKED && sizeof(T) == 4;
-  Picks out{-1, false};
-  if (p.n_group > 1) {
-    // 64 / n_group lanes (a power of two) a group: each finds the best two of its
-    // part, a butterfly joins them
+// The best two of all keys of this lane's group, from those of a lane, a >= b; the
+// group's score.
+template <typename T>
+__device__ __forceinline__ auto group_score(const RouteParams& p, T a, T b, int lanes) {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (64 * j + lane < p.E) lds[64 * j + lane] = key[j];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    const int lanes = 1 << (31 - __builtin_clz(uint32_t(kWave / p.n_group)));
-    const int group = lane / lanes, sub = lane % lanes;
-    T a = kNone<T>, b = kNone<T>;  // a >= b
-    if (group < p.n_group) {
-      for (int i = sub; i < p.size; i += lanes) {
-        const T v = lds[group * p.size + i];
-        b = v > a ? a : (v > b ? v : b);
-        a = v > a ? v : a;
-      }
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      if (o >= lanes) continue;
-      const T c = partner(a, o), d = partner(b, o);
-      const T low = c > a ? a : c;
-      a = c > a ? c : a;
-      const T high = d > b ? d : b;
-      b = low > high ? low : high;
-    }
-    if (p.group_top == 2 && b > kNone<T>) a += b;
-    // a group's rank, and the scores on both sides of the cut
-    int rank = 0;
-    for (int g = 0; g < p.n_group; ++g) {
-      const T v = from_lane(a, g * lanes);
-      rank += v > a || (v == a && g < group);
-    }
-    const uint64_t kept = __ballot(sub == 0 && group < p.n_group && rank < p.topk_group);
-    if (kCheck && p.topk_group < p.n_group) {
-      const uint64_t in = __ballot(sub == 0 && group < p.n_group && rank == p.topk_group - 1);
-      const uint64_t next = __ballot(sub == 0 && group < p.n_group && rank == p.topk_group);
-      if (open_between(from_lane(a, __builtin_ctzll(in)), from_lane(a, __builtin_ctzll(next)))) {
-        out.open = true;
-        return out;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint32_t e = 64 * j + lane;
-      const uint32_t g = e * p.inv_size >> 20;
-      if (e < uint32_t(p.E) && !(kept >> (g * lanes) & 1)) key[j] = kNone<T>;
+  for (int o = 32; o > 0; o >>= 1) {
+    if (o >= lanes) continue;
+    const T c = partner(a, o), d = partner(b, o);
+    const T low = c > a ? a : c, high = d > b ? d : b;
+    a = c > a ? c : a;
+    b = low > high ? low : high;
+  }
+  const auto s = value_of(a);
+  return p.group_top == 2 && b > none<T>() ? s + value_of(b) : s;
+}
+
+// What another lane of this wavefront wrote to LDS before is read behind this.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The groups' ranks from keys in LDS, 64 / n_group lanes (a power of two) a group.
+// Returns whether the cut is open; *kept has the bit of expert e's group at (its
+// number << shift).
+template <typename T>
+__device__ __forceinline__ bool groups_in_lds(const RouteParams& p, const T* lds, int shift, uint64_t* kept) {
+  const int lane = lane_id(), lanes = 1 << shift, group = lane >> shift;
+  T a = none<T>(), b = none<T>();
+  if (group < p.n_group) {
+    for (int i = lane & (lanes - 1); i < p.size; i += lanes) {
+      const T v = lds[group * p.size + i];
+      b = v > a ? a : (v > b ? v : b);
+      a = v > a ? v : a;
     }
   }
-  // each lane's keys in descending order, equal ones as they were
+  int rank;
+  const bool open = rank_groups(p, group_score(p, a, b, lanes), group, lanes, &rank);
+  *kept = __ballot(rank < p.topk_group);
+  return open;
+}
+__device__ __forceinline__ int group_lane_shift(const RouteParams& p) {
+  return 31 - __builtin_clz(uint32_t(kWave / p.n_group));
+}
+
+// Picks by `key`; key[j] is expert V lane + j's.  The r-th goes to *id of lane
+// `first` + r.  Returns whether some decision is left open; then *id may hold
+// anything in these lanes.
+template <int V, bool kCheck>
+__device__ __forceinline__ bool pick(const RouteParams& p, uint32_t (&key)[V], uint32_t* lds, int first, int* id) {
+  using T = uint32_t;
+  const int lane = lane_id();
+  // compared where they are needed: kept as masks across rows they would fill the
+  // scalar registers
+  int E = p.E, group_shift = p.group_shift, topk = p.topk;
+  asm volatile("" : "+s"(E), "+s"(group_shift), "+s"(topk));
+  // groups of a power of two lanes need no exchange through LDS
+  const bool whole = group_shift >= 0;
+  if (p.n_group > 1 && !whole) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (V * lane + j < E) lds[V * lane + j] = key[j];
+    wave_sync();
+    const int shift = group_lane_shift(p);
+    uint64_t kept;
+    if (groups_in_lds(p, lds, shift, &kept) && kCheck) return true;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const uint32_t e = V * lane + j, g = e * p.inv_size >> 20;
+      if (e < uint32_t(E) && !(kept >> (g << shift) & 1)) key[j] = none<T>();
+    }
+    wave_sync();  // the next row's keys go there
+  }
+  // this lane's keys in descending order, equal ones as they were, and where they
+  // were, four bits each
   int at[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) at[j] = j;
@@ -164,153 +238,315 @@ __device__ __forceinline__ Picks pick(const RouteParams& p, T (&key)[V], T* lds)
       at[j] = swap ? at[j + 1] : t;
       at[j + 1] = swap ? t : at[j + 1];
     }
-  T last = kNone<T>;
-  for (int r = 0; r < p.topk + (kCheck ? 1 : 0); ++r) {
-    const T top = from_lane(wave_max(key[0]), 0);  // (a scalar)
-    if (!(top > kNone<T>)) break;
-    if (kCheck && r > 0 && open_between(last, top)) {
-      out.open = true;
-      return out;
-    }
-    if (r == p.topk) break;
-    const uint64_t equal = __ballot(key[0] == top);
-    int win = __builtin_ctzll(equal);
-    if (equal & (equal - 1)) {  // the lowest index: the lowest of `at`, then of the lanes
+  constexpr int kWords = (V + 7) / 8;
+  uint32_t where[kWords] = {};
 #pragma unroll
-      for (int j = V - 1; j >= 0; --j) {
-        const uint64_t here = __ballot(key[0] == top && at[0] == j);
-        if (here) win = __builtin_ctzll(here);
-      }
-    }
-    const int id = 64 * __builtin_amdgcn_readlane(at[0], win) + win;
-    if (lane == r) out.id = id;
-    if (lane == win) {
+  for (int j = 0; j < V; ++j) where[j / 8] |= uint32_t(at[j]) << 4 * (j % 8);
+  if (p.n_group > 1 && whole) {
+    const int lanes = 1 << group_shift, group = lane >> group_shift;
+    int rank;
+    const bool open = rank_groups(p, group_score(p, key[0], V > 1 ? key[V > 1] : none<T>(), lanes), group, lanes,
+                                  &rank);
+    if (open && kCheck) return true;
 #pragma unroll
-      for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1], at[j] = at[j + 1];
-      key[V - 1] = kNone<T>;
-    }
-    last = top;
+    for (int j = 0; j < V; ++j) key[j] = rank < p.topk_group ? key[j] : none<T>();
   }
-  return out;
+  T mine = none<T>(), beyond = none<T>();
+  asm volatile("" : "+s"(topk));
+  int r = 0;
+  for (; r < topk; ++r) {
+    const T top = wave_max(key[0]);
+    if (!(top > none<T>())) break;
+    const int win = __builtin_ctzll(__ballot(key[0] == top));
+    const int e = V * win + int(uint32_t(__builtin_amdgcn_readlane(int(where[0]), win)) & 15);
+    const bool here = lane == first + r;
+    *id = here ? e : *id;
+    if constexpr (kCheck) mine = here ? top : mine;
+    const bool step = lane == win;
+#pragma unroll
+    for (int j = 0; j < V; ++j) key[j] = step ? (j + 1 < V ? key[j + 1 < V ? j + 1 : j] : none<T>()) : key[j];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      uint32_t n = where[i] >> 4;
+      if (i + 1 < kWords) n |= where[i + 1 < kWords ? i + 1 : i] << 28;
+      where[i] = step ? n : where[i];
+    }
+  }
+  if constexpr (kCheck) {
+    if (r == topk) beyond = wave_max(key[0]);
+    const T next = lane == first + topk - 1 ? beyond : __shfl_down(mine, 1);
+    return __ballot(uint32_t(lane - first) < uint32_t(topk) && open_between(value_of(mine), value_of(next), p.sigmoid));
+  }
+  return false;
 }
 
-// Keys that are scores (plus bias), in T.
-template <typename T, int V>
-__device__ __forceinline__ bool score_keys(const RouteParams& p, const float (&x)[V], float m, T (&key)[V]) {
-  const int lane = lane_id();
-  T s[V], sum = 0;
+// Keys that are scores (plus bias); whether an unmasked one is NaN.
+template <int V>
+__device__ __forceinline__ bool score_keys(const RouteParams& p, const float (&x)[V], const float (&bias)[V],
+                                           float m, uint32_t (&key)[V]) {
+  float s[V], sum = 0;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     // a masked or missing expert has no share
-    s[j] = !(x[j] > kNone<float>) ? T(0) : p.sigmoid ? T(1) / (T(1) + exp_of(-T(x[j]))) : exp_from(T(x[j]), T(m));
+    const float v = p.sigmoid ? over_one(1.0f + exp_of(-x[j])) : exp_from(x[j], m);
+    s[j] = x[j] > kMasked ? v : 0.0f;
     sum += s[j];
   }
   if (!p.sigmoid) {
-    sum = wave_sum(sum);
+    sum = over_one(sum_over(sum, kWave));
 #pragma unroll
-    for (int j = 0; j < V; ++j) s[j] /= sum;
+    for (int j = 0; j < V; ++j) s[j] *= sum;
   }
   bool nan = false;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int e = 64 * j + lane;
-    key[j] = s[j];
-    if (p.bias && e < p.E) key[j] += T(p.bias[e]);
-    const bool live = x[j] > kNone<float>;
-    nan |= live && key[j] != key[j];
-    if (!live || key[j] != key[j]) key[j] = kNone<T>;
+    const float v = x[j] > kMasked ? s[j] + bias[j] : kMasked;
+    nan |= v != v;
+    key[j] = key_of<uint32_t>(v);
   }
   return nan;
 }
 
-template <typename X, int V, bool BY_SCORE>
-__device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, double* lds) {
-  const int lane = lane_id();
-  const X* logits = reinterpret_cast<const X*>(p.logits) + row * p.E;
-  auto logit = [&](int e) {
-    if constexpr (sizeof(X) == 2)
-      return bf16_to_f32(logits[e]);
-    else
-      return logits[e];
-  };
-  float x[V];
-  bool nan = false;
-  float m = kNone<float>;
+// A row's logits, V consecutive ones a lane; what is not there is -infinity.
+template <typename X, int V>
+__device__ __forceinline__ void load_row(const RouteParams& p, const X* row, float (&x)[V]) {
+  int e = V * lane_id();
+  asm volatile("" : "+v"(e));  // addresses are not to be kept across rows: they take registers
+  if (p.vectors) {  // (E is a multiple of V)
+    constexpr int kBytes = V * int(sizeof(X)), kWords = (kBytes + 3) / 4;
+    uint32_t q[kWords];
+    const X* from = row + min(e, p.E - V);
+    if constexpr (kBytes == 2) q[0] = *from;
+    if constexpr (kBytes == 4) q[0] = *reinterpret_cast<const uint32_t*>(from);
+    if constexpr (kBytes == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(from);
+      q[0] = v.x, q[1] = v.y;
+    }
+    if constexpr (kBytes >= 16) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = 64 * j + lane;
-    x[j] = e < p.E ? logit(e) : kNone<float>;
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = reinterpret_cast<const uint4*>(from)[i / 4];
+        q[i] = v.x, q[i + 1] = v.y, q[i + 2] = v.z, q[i + 3] = v.w;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float v = sizeof(X) == 4 ? __uint_as_float(q[j * sizeof(X) / 4])
+                                     : __uint_as_float(j % 2 ? q[j / 2] & 0xffff0000u : q[j / 2] << 16);
+      x[j] = e < p.E ? v : kMasked;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const X v = row[min(e + j, p.E - 1)];
+      x[j] = e + j >= p.E ? kMasked : sizeof(X) == 4 ? float(v) : bf16_to_f32(uint16_t(v));
+    }
   }
+}
+
+// What a lane holds between a row's picking and the weighing: its pick, and of the
+// pick's row the largest logit, the sum of the softmax and whether there was NaN.
+struct Lane {
+  int id;
+  float m, sum;
+  bool nan;
+};
+
+// Picks of a row, into lanes first .. first + topk - 1 (`mine`: whether this is one).
+// Returns whether fp32 leaves some open.
+template <typename X, int V, bool BY_SCORE>
+__device__ __forceinline__ bool pick_row(const RouteParams& p, const float (&x)[V], const float (&bias)[V],
+                                         double* lds, int first, bool mine, Lane* out) {
+  bool nan = false, open = false;
+  uint32_t top = none<uint32_t>();
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     nan |= x[j] != x[j];
-    if (x[j] != x[j]) x[j] = kNone<float>;  // never picked
-    m = x[j] > m ? x[j] : m;
+    if (!p.sigmoid && (BY_SCORE || !p.renorm)) top = max(top, key_of<uint32_t>(x[j] + 0.0f));
   }
-  m = wave_max(m);
-  Picks picks;
+  // the largest logit, where scores are relative to it
+  const float m = !p.sigmoid && (BY_SCORE || !p.renorm) ? value_of(wave_max(top)) : 0.0f;
   if constexpr (BY_SCORE) {
-    float key[V];
-    nan |= score_keys(p, x, m, key);
-    picks = pick<float, V, true>(p, key, reinterpret_cast<float*>(lds));
-    if (picks.open) {
-      double wide[V];
-      score_keys(p, x, m, wide);
-      picks = pick<double, V, true>(p, wide, lds);
-    }
+    uint32_t key[V];
+    nan |= score_keys(p, x, bias, m, key);
+    open = pick<V, true>(p, key, reinterpret_cast<uint32_t*>(lds), first, &out->id);
   } else {
-    float key[V];
+    uint32_t key[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = x[j];
-    picks = pick<float, V, false>(p, key, reinterpret_cast<float*>(lds));
+    for (int j = 0; j < V; ++j) key[j] = key_of<uint32_t>(x[j] + 0.0f);  // (both zeros are one)
+    pick<V, false>(p, key, reinterpret_cast<uint32_t*>(lds), first, &out->id);
   }
-
-  // The weights, a pick a lane.  Renormalised, the common factor cancels, and
-  // everything is relative to the largest of the picks, so that none underflows.
-  const bool have = picks.id >= 0;
-  const float xr = have ? logit(picks.id) : kNone<float>;
-  float s = 0.0f;
-  if (p.renorm) {
-    const float top = wave_max(xr);
-    if (have) {
-      if (!p.sigmoid) {
-        s = exp_from(xr, top);
-      } else if (xr > 0.0f) {
-        s = 1.0f / (1.0f + expf(-xr));
-      } else {
-        s = exp_from(xr, fminf(top, 0.0f)) / (1.0f + expf(xr));
-      }
-    }
-    const float sum = wave_sum(s);
-    if (sum > 0.0f) s /= sum;
-  } else if (p.sigmoid) {
-    if (have) s = xr > 0.0f ? 1.0f / (1.0f + expf(-xr)) : expf(xr) / (1.0f + expf(xr));
-  } else {
+  const bool bad = __ballot(nan) != 0;
+  out->nan = mine ? bad : out->nan;
+  if (!p.sigmoid && !p.renorm) {
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum += x[j] > kNone<float> ? exp_from(x[j], m) : 0.0f;
-    sum = wave_sum(sum);
-    if (have) s = exp_from(xr, m) / sum;
+    for (int j = 0; j < V; ++j) {
+      sum += x[j] > kMasked ? exact_exp_from(x[j], m) : 0.0f;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    sum = sum_over(sum, kWave);
+    out->m = mine ? m : out->m;
+    out->sum = mine ? sum : out->sum;
   }
-  s *= p.scale;
-  if (__ballot(nan)) s = __builtin_nanf("");
-  if (lane < p.topk) {
-    p.ids[row * p.topk + lane] = picks.id;
-    p.weights[row * p.topk + lane] = s;
+  return open;
+}
+
+// The same picks in fp64.  Few rows come here: an expert at a time, the keys in
+// LDS, so that it takes no more registers than the rest.
+template <typename X>
+__device__ __forceinline__ void pick_again(const RouteParams& p, const X* row, double* lds, int first, bool mine,
+                                           Lane* out) {
+  const int lane = lane_id();
+  auto logit = [&](int e) {
+    if constexpr (sizeof(X) == 4)
+      return row[e];
+    else
+      return bf16_to_f32(row[e]);
+  };
+  uint32_t top = none<uint32_t>();
+#pragma unroll 1
+  for (int e = lane; e < p.E; e += kWave) top = max(top, key_of<uint32_t>(logit(e) + 0.0f));
+  const double m = value_of(wave_max(top));
+  double sum = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < p.E; e += kWave) {
+    const float x = logit(e);
+    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-double(x))) : exp_from(double(x), m);
+    lds[e] = x > kMasked ? s : none<double>();
+    sum += x > kMasked ? s : 0.0;
+  }
+  sum = p.sigmoid ? 1.0 : sum_over(sum, kWave);
+#pragma unroll 1
+  for (int e = lane; e < p.E; e += kWave) {
+    const double s = lds[e];
+    lds[e] = s > none<double>() ? key_of<double>(s / sum + (p.bias ? double(p.bias[e]) : 0.0)) : s;
+  }
+  wave_sync();
+  if (p.n_group > 1) {
+    const int shift = group_lane_shift(p);
+    uint64_t kept;
+    groups_in_lds(p, lds, shift, &kept);
+    wave_sync();
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += kWave)
+      if (!(kept >> (uint32_t(e) * p.inv_size >> 20 << shift) & 1)) lds[e] = none<double>();
+    wave_sync();
+  }
+  out->id = mine ? -1 : out->id;
+  for (int r = 0; r < p.topk; ++r) {
+    double best = none<double>();
+    uint32_t at = 0;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += kWave) {
+      const double v = lds[e];
+      at = v > best ? uint32_t(e) : at;
+      best = v > best ? v : best;
+    }
+    const double most = wave_max(best);
+    if (!(most > none<double>())) break;
+    const int e = int(~wave_max(best == most ? ~at : 0u));  // the lowest of equal ones
+    out->id = lane == first + r ? e : out->id;
+    if (lane == 0) lds[e] = none<double>();
+    wave_sync();
   }
 }
 
+// The weights of `rows` rows, a pick a lane, 2^each lanes a row.
+// Renormalised, the common factor cancels, and everything is relative to the
+// largest of the row's picks, so that none underflows.
+template <typename X>
+__device__ __forceinline__ void weigh_rows(const RouteParams& p, int64_t row0, int rows, int each, const Lane& in) {
+  const int lane = lane_id(), q = lane >> each, r = lane & ((1 << each) - 1);
+  const int64_t row = row0 + q;
+  const bool have = in.id >= 0;
+  float x = kMasked;
+  if (have) {
+    const X v = (reinterpret_cast<const X*>(p.logits) + row * p.E)[in.id];
+    x = sizeof(X) == 4 ? float(v) : bf16_to_f32(uint16_t(v));
+  }
+  float s = 0.0f;
+  if (p.renorm) {
+    float ref = x;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+      if (o < 1 << each) ref = fmaxf(ref, partner(ref, o));
+    if (have) {
+      if (!p.sigmoid) {
+        s = exact_exp_from(x, ref);
+      } else if (x > 0.0f) {
+        s = 1.0f / (1.0f + expf(-x));
+      } else {
+        s = exact_exp_from(x, fminf(ref, 0.0f)) / (1.0f + expf(x));
+      }
+    }
+    const float sum = sum_over(s, 1 << each);
+    if (sum > 0.0f) s /= sum;
+  } else if (have) {
+    if (!p.sigmoid)
+      s = exact_exp_from(x, in.m) / in.sum;
+    else
+      s = x > 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x) / (1.0f + expf(x));
+  }
+  s *= p.scale;
+  if (in.nan) s = __builtin_nanf("");
+  if (r < p.topk && q < rows) {
+    p.ids[row * p.topk + r] = in.id;
+    p.weights[row * p.topk + r] = s;
+  }
+}
+
+// Each wavefront takes p.batch rows in a row, as many as have their picks in its
+// lanes at once, then weighs them together, and goes on to others.
 template <typename X, int V, bool BY_SCORE>
 __global__ void __launch_bounds__(kWaves * kWave) route_kernel(RouteParams p) {
   __shared__ double lds[kWaves][BY_SCORE ? 64 * V : 32 * V];
-  const int w = wave_id();
-  for (int64_t row = int64_t(blockIdx.x) * kWaves + w; row < p.M; row += int64_t(gridDim.x) * kWaves)
-    route_row<X, V, BY_SCORE>(p, row, lds[w]);
+  const int lane = lane_id(), w = wave_id(), each = p.slot_shift;
+  const X* logits = reinterpret_cast<const X*>(p.logits);
+  const int64_t step = int64_t(gridDim.x) * kWaves * p.batch;
+  int64_t row0 = (int64_t(blockIdx.x) * kWaves + w) * p.batch;
+  if (row0 >= p.M) return;
+  float bias[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) bias[j] = BY_SCORE && p.bias ? p.bias[min(V * lane + j, p.E - 1)] : 0.0f;
+  float x[V], next[V];
+  load_row<X, V>(p, logits + row0 * p.E, x);
+  for (; row0 < p.M; row0 += step) {
+    const int rows = int(std::min<int64_t>(p.batch, p.M - row0));
+    Lane out{-1, 0.0f, 1.0f, false};
+    uint64_t open = 0;  // rows to be done again
+    for (int q = 0; q < rows; ++q) {
+      // (behind the last row of all: one that is there)
+      const int64_t ahead = q + 1 < rows ? row0 + q + 1 : row0 + step < p.M ? row0 + step : row0;
+      load_row<X, V>(p, logits + ahead * p.E, next);
+      const bool again = pick_row<X, V, BY_SCORE>(p, x, bias, lds[w], q << each, lane >> each == q, &out);
+      if (BY_SCORE && again) open |= uint64_t(1) << q;
+#pragma unroll
+      for (int j = 0; j < V; ++j) x[j] = next[j];
+    }
+    if constexpr (BY_SCORE) {
+      for (; open; open &= open - 1) {
+        const int q = __builtin_ctzll(open);
+        pick_again(p, logits + (row0 + q) * p.E, lds[w], q << each, lane >> each == q, &out);
+      }
+    }
+    weigh_rows<X>(p, row0, rows, each, out);
+  }
 }
+
 template <typename X, int V>
-hipError_t route_launch(const RouteParams& p, hipStream_t st) {
-  // (a launch has fewer than 2^32 threads: beyond that a wavefront takes several rows)
-  const dim3 grid(unsigned(std::min<int64_t>((p.M + kWaves - 1) / kWaves, 1 << 22))), block(kWaves * kWave);
+hipError_t route_launch(RouteParams p, hipStream_t st) {
+  p.vectors = p.E % V == 0 && reinterpret_cast<uintptr_t>(p.logits) % std::min<size_t>(16, V * sizeof(X)) == 0;
+  const int lanes = p.size / V;
+  p.group_shift = p.size % V == 0 && (lanes & (lanes - 1)) == 0 ? __builtin_ctz(lanes) : -1;
+  // Rows whose picks a wavefront has room for, and how many of them it takes: with
+  // few rows one, for the sake of the others.
+  p.slot_shift = 0;
+  while (1 << p.slot_shift < p.topk) ++p.slot_shift;
+  const int64_t waves = int64_t(std::max(xcd_compute_units(), 1)) * kXcds * 16;
+  p.batch = int32_t(std::min<int64_t>(kWave >> p.slot_shift, std::max<int64_t>(1, p.M / waves)));
+  const int64_t want = (p.M + int64_t(p.batch) * kWaves - 1) / (int64_t(p.batch) * kWaves);
+  const dim3 grid(unsigned(std::min(want, 8 * waves))), block(kWaves * kWave);
   if (p.bias || p.group_top == 2)
     hipLaunchKernelGGL((route_kernel<X, V, true>), grid, block, 0, st, p);
   else
