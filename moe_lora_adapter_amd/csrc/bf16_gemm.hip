@@ -379,13 +379,13 @@ __global__ void __launch_bounds__(kSplit * kWave) gemm_rows_kernel(ProductParams
 //
 // KG > 1, for small tiles: a stage has KG blocks of 64, each of which WM x WN
 // wavefronts multiply, and their sums meet in LDS.
-template <int WM, int WN, int FM, int FN, int NS, int KG = 1>
+template <int WM, int WN, int FM, int FN, int NS, int KS = 1, int KG = 1>
 struct Tile {
   static constexpr int BM = WM * FM * 16, BN = WN * FN * 16, NW = WM * WN * KG;
   static constexpr int XI = BM / 8 / NW, WI = BN / 8 / NW;  // 1 KiB loads a wavefront and K block
-  static constexpr int kEach = XI + WI, kLoads = KG * kEach;
+  static constexpr int kEach = XI + WI, kLoads = KS * KG * kEach;
   static constexpr int kX = 0, kW = BM * 128, kBlock = kW + BN * 128;
-  static constexpr int kStage = KG * kBlock;
+  static constexpr int kStage = KS * KG * kBlock;
   static constexpr int kJoin = NS * kStage;  // (KG > 1) sums of the other wavefronts
   // the rows' pairs and weights of the tile being stored, of those whose stages
   // are in the ring (one each where K is one block), and of the next to load
@@ -402,16 +402,15 @@ struct Tile {
   static_assert(BM <= NW * kWave && FM % 2 == 0 && FN % 2 == 0 && NS >= 2, "tile");
 };
 
-template <int WM, int WN, int FM, int FN, int NS, bool GROUPED, int KG>
+template <int WM, int WN, int FM, int FN, int NS, bool GROUPED, int KS, int KG>
 __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
     gemm_tile_kernel(ProductParams p, int ntiles) {
-  using T = Tile<WM, WN, FM, FN, NS, KG>;
+  using T = Tile<WM, WN, FM, FN, NS, KS, KG>;
   constexpr int BM = T::BM, BN = T::BN, XI = T::XI, WI = T::WI, kLoads = T::kLoads;
-  constexpr bool kPhases = FM > 2;  // (below)
-  static_assert(KG == 1 || (!GROUPED && !kPhases), "a stage of several K blocks");
-  static_assert(!kPhases || NS == 2, "phases");
+  constexpr bool kPhases = KS == 1;  // (below)
+  static_assert(!GROUPED || KS * KG == 1, "a stage of several K blocks");
   constexpr int kX = T::kX, kW = T::kW, kStage = T::kStage;
-  const int stages = (p.KB + KG - 1) / KG;  // of a tile
+  const int stages = (p.KB + KS * KG - 1) / (KS * KG);  // of a tile
   __shared__ __align__(1024) uint8_t lds[T::lds_bytes(GROUPED)];
 
   TileList* list = reinterpret_cast<TileList*>(lds + T::kList);
@@ -445,13 +444,14 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
   // anywhere: lane i keeps the offset of this wavefront's row i.  The columns'
   // chunk order has two forms, by bit 3 of the column.
   const int xc = 16 * (cl ^ rl), wc = 16 * (cl ^ swizzle(rl));
-  uint32_t xoff, woff, woff1;
+  uint32_t xoff[XI], woff[WI];  // of each of a block's loads
+  auto chunk_flip = [&](int l) { return 16 * swizzle(8 * (w * WI + l)); };  // of a load of columns
   const uint32_t xstep = 8 * K2, wstep = gated ? 4 * K2 : 8 * K2;
   const uint32_t base = lds_address(lds);
   int2* pairs = reinterpret_cast<int2*>(lds + T::kPairs);
 
   auto set_tile = [&]() {
-    uint32_t nx = kOob, nw = kOob, nw1 = kOob;  // nothing left: loads from nowhere
+    uint32_t nx = kOob, nw = kOob;  // nothing left: loads from nowhere
     if (lt < items.end) {
       // not to be computed once and kept: the registers are needed
       int ln = lane;
@@ -495,34 +495,31 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
       const uint32_t n = gated ? tile * (BN / 2) + 4 * w * WI + (r & 3) + (r >> 2) * p.No
                                : tile * BN + 8 * w * WI + r;
       nw = n * K2;
-      nw1 = nw + (wc ^ 64);
-      nw += wc;
     }
-    xoff = nx;
-    woff = nw;
-    woff1 = nw1;
+    each<XI>([&](auto l) {
+      xoff[l] = GROUPED ? __builtin_amdgcn_ds_bpermute(4 * (8 * l + rl), nx) + xc : nx + uint32_t(l) * xstep;
+    });
+    each<WI>([&](auto l) { woff[l] = nw + uint32_t(l) * wstep + (wc ^ chunk_flip(l)); });
   };
   // One of a stage's loads.  Chunks past K in a short last block read as
   // zeros; behind the last tile everything does, so that every stage counts the
   // same loads.
-  auto load = [&](int l) {
-    const int kb = KG == 1 ? lkb : lkb * KG + l / T::kEach;
-    const uint32_t st = base + uint32_t(lstage) * kStage + uint32_t(l / T::kEach * T::kBlock);
-    l %= T::kEach;
-    // (a stage's second block may be past K)
-    const uint32_t k = kb < p.KB ? uint32_t(kb) * (2 * kStageK) : 0;
-    const int have = kb < p.KB ? int(K2 - k) : 0;
-    if (l < XI) {
-      const uint32_t o = GROUPED ? __builtin_amdgcn_ds_bpermute(4 * (8 * l + rl), xoff) + xc
-                                 : xoff + uint32_t(l) * xstep;
-      tile_dma16(xr, st + kX + 1024 * (w * XI + l), xc < have ? o : kOob, k);
-    } else {
-      const int i = l - XI;
-      const int flip = 16 * swizzle(8 * (w * WI + i));
-      tile_dma16(wr, st + kW + 1024 * (w * WI + i),
-                 (wc ^ flip) < have ? (flip ? woff1 : woff) + uint32_t(i) * wstep : kOob, k);
-    }
+  auto load = [&](auto at) {
+    constexpr int block = at / T::kEach, l = at % T::kEach;
+    const int kb = lkb * (KS * KG) + block;
+    const uint32_t st = base + uint32_t(lstage) * kStage + uint32_t(block * T::kBlock);
+    // (a stage's later blocks may be past K)
+    const uint32_t k = KS * KG == 1 || kb < p.KB ? uint32_t(kb) * (2 * kStageK) : 0;
+    const int have = KS * KG == 1 || kb < p.KB ? int(K2 - k) : 0;
+    if constexpr (l < XI)
+      tile_dma16(xr, st + kX + 1024 * (w * XI + l), xc < have ? xoff[l] : kOob, k);
+    else
+      tile_dma16(wr, st + kW + 1024 * (w * WI + l - XI), (wc ^ chunk_flip(l - XI)) < have ? woff[l - XI] : kOob, k);
   };
+  constexpr int kXLoads = KS * KG * XI, kWLoads = KS * KG * WI;
+  // (with phases a stage's columns are loaded before its rows)
+  auto load_x = [&](auto q) { load(std::integral_constant<int, q / XI * T::kEach + q % XI>{}); };
+  auto load_w = [&](auto q) { load(std::integral_constant<int, q / WI * T::kEach + XI + q % WI>{}); };
   auto loaded = [&]() {  // a stage's loads are all issued
     ++lkb;
     lstage = lstage + 1 == NS ? 0 : lstage + 1;
@@ -544,8 +541,8 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
   set_tile();
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
-#pragma unroll
-    for (int l = 0; l < kLoads; ++l) load(kPhases ? (l + XI) % kLoads : l);
+    each<kWLoads>(load_w);
+    each<kXLoads>(load_x);
     loaded();
     if (lkb == stages) next_loads();
   }
@@ -570,16 +567,13 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
     if (none) {
       for (int kb = 0; kb < stages; ++kb) {
         if constexpr (kPhases) {
-          stage_barrier<XI>();
-#pragma unroll
-          for (int l = XI; l < XI + WI; ++l) load(l);
-          stage_barrier<WI>();
-#pragma unroll
-          for (int l = 0; l < XI; ++l) load(l);
+          stage_barrier<kWait + kXLoads>();
+          each<kWLoads>(load_w);
+          stage_barrier<kWait + kWLoads>();
+          each<kXLoads>(load_x);
         } else {
           stage_barrier<kWait>();
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) load(l);
+          each<kLoads>([&](auto l) { load(l); });
         }
         loaded();
         stage = stage + 1 == NS ? 0 : stage + 1;
@@ -602,7 +596,7 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
       // load has a whole stage to arrive.  4096 x 4096 x 12288: 289 us, 301 with one
       // barrier a stage and the columns' reads behind it; 1 step ahead 295; four
       // wavefronts of 128 x 128 each 303.
-      constexpr int kAhead = 2, kHeld = 4, kSteps = 2 * FM;
+      constexpr int kAhead = FM > 2 ? 2 : 1, kHeld = 4, kSteps = 2 * FM;
       uint4 wf[2][FN], xf[kHeld];
       auto columns = [&](const uint8_t* st, auto h, auto f) {
         constexpr int o = 4096 * (f >> 1) + 512 * (f & 1);
@@ -622,8 +616,8 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
           const uint8_t* nx = lds + stage * kStage;
           each<kSteps>([&](auto step) {
             constexpr int s = step, h = s / FM, i = s % FM, ahead = s + kAhead;
-            if constexpr (s == FM) stage_barrier<XI>();
-            if constexpr (ahead == kSteps) stage_barrier<WI>();
+            if constexpr (s == FM) stage_barrier<kWait + kXLoads>();
+            if constexpr (ahead == kSteps) stage_barrier<kWait + kWLoads>();
             rows(ahead < kSteps ? st : nx, std::integral_constant<int, ahead % kSteps>{});
             each<FN>([&](auto f) {
               acc[i][f] = mfma_bf16(wf[h][f], xf[s % kHeld], acc[i][f]);
@@ -633,11 +627,11 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
                 if constexpr (slot == kRead * c / FN) columns(h ? nx : st, std::integral_constant<int, 1 - h>{}, c);
               });
               if constexpr (h == 1) {
-                each<WI>([&](auto l) {
-                  if constexpr (slot == 1 + (kRead - 1) * l / WI) load(XI + l);
+                each<kWLoads>([&](auto l) {
+                  if constexpr (slot == 1 + (kRead - 1) * l / kWLoads) load_w(l);
                 });
-                each<XI>([&](auto l) {
-                  if constexpr (slot == kRead + kAhead * FN * l / XI) load(l);
+                each<kXLoads>([&](auto l) {
+                  if constexpr (slot == kRead + kAhead * FN * l / kXLoads) load_x(l);
                 });
               }
               __builtin_amdgcn_sched_barrier(0);
@@ -649,48 +643,49 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
         if (lkb == stages) next_loads();
       }
     } else {
-      // A stage is FM steps of 2 FN MFMAs: a step reads the next one's rows.  The
-      // stage's barrier stands before the last step, once every wavefront has its
-      // last rows of the stage in registers; behind it the stage's buffer is
-      // refilled, and each column operand is replaced by the next stage's after its
-      // last use.
-      uint4 wf[2][FN], xf[2][2];
-      auto columns = [&](const uint8_t* st, auto h, auto f) {
-        constexpr int o = 4096 * (f >> 1) + 512 * (f & 1);
-        wf[h][f] = *reinterpret_cast<const uint4*>(st + (h ? wo ^ 64 : wo) + o);
+      // A wavefront has the operands of a K block in registers and reads those of the
+      // next while it multiplies.  Before the last block of a stage stands the
+      // stage's barrier: every wavefront has read it, and the next one has to be
+      // there; behind it the stage's buffer is refilled.  What a stage costs besides
+      // its MFMAs is that barrier and the latency behind it: KS > 1 blocks share it.
+      uint4 wf[2][2][FN], xf[2][2][FM];
+      auto read = [&](const uint8_t* st, auto set, auto block) {
+        each<2 * FN>([&](auto j) {
+          constexpr int h = j / FN, f = j % FN, o = block * KG * T::kBlock + 4096 * (f >> 1) + 512 * (f & 1);
+          wf[set][h][f] = *reinterpret_cast<const uint4*>(st + (h ? wo ^ 64 : wo) + o);
+        });
+        each<2 * FM>([&](auto j) {
+          constexpr int h = j / FM, i = j % FM, o = block * KG * T::kBlock + 2048 * i;
+          xf[set][h][i] = *reinterpret_cast<const uint4*>(st + (h ? xo ^ 64 : xo) + o);
+        });
       };
-      auto rows = [&](const uint8_t* st, auto i) {
-        xf[i & 1][0] = *reinterpret_cast<const uint4*>(st + xo + 2048 * i);
-        xf[i & 1][1] = *reinterpret_cast<const uint4*>(st + (xo ^ 64) + 2048 * i);
-      };
-      constexpr std::integral_constant<int, 0> first;
-      each<2 * FN>([&](auto j) {
-        columns(lds + stage * kStage, std::integral_constant<int, j / FN>{}, std::integral_constant<int, j % FN>{});
-      });
-      rows(lds + stage * kStage, first);
+      static_assert(kPhases || KS % 2 == 0, "the sets take turns");
+      read(lds + stage * kStage, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
       for (int kb = 0; kb < stages;) {
         const int n = std::min(stages - kb, stages - lkb);
         for (int r = 0; r < n; ++r) {
           const uint8_t* st = lds + stage * kStage;
           stage = stage + 1 == NS ? 0 : stage + 1;
           const uint8_t* nx = lds + stage * kStage;
-          each<FM>([&](auto i) {
-            constexpr bool last = i == FM - 1;
+          each<KS>([&](auto block) {
+            constexpr int set = block % 2;
+            constexpr bool last = block == KS - 1;
+            constexpr std::integral_constant<int, 1 - set> other;
             if constexpr (last) {
               stage_barrier<kWait>();
-              rows(nx, first);
+              read(nx, other, std::integral_constant<int, 0>{});
             } else {
-              rows(st, std::integral_constant<int, i + 1>{});
+              read(st, other, std::integral_constant<int, block + 1>{});
             }
-            each<2 * FN>([&](auto j) {
-              constexpr int h = j / FN, f = j % FN;
-              acc[i][f] = mfma_bf16(wf[h][f], xf[i & 1][h], acc[i][f]);
-              if constexpr (last) {
-                columns(nx, std::integral_constant<int, h>{}, std::integral_constant<int, f>{});
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int kAll = 2 * FM * FN;
+            each<kAll>([&](auto j) {
+              constexpr int h = j / (FM * FN), i = j / FN % FM, f = j % FN;
+              acc[i][f] = mfma_bf16(wf[set][h][f], xf[set][h][i], acc[i][f]);
+              if constexpr (last)
                 each<kLoads>([&](auto l) {
-                  if constexpr (l >= kLoads * j / (2 * FN) && l < kLoads * (j + 1) / (2 * FN)) load(l);
+                  if constexpr (l >= kLoads * j / kAll && l < kLoads * (j + 1) / kAll) load(l);
                 });
-              }
               __builtin_amdgcn_sched_barrier(0);
             });
           });
@@ -740,9 +735,9 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
 int own_columns(const ProductParams& p, int cols) { return p.gated ? cols / 2 : cols; }
 int column_tiles(const ProductParams& p, int cols) { return (p.No + own_columns(p, cols) - 1) / own_columns(p, cols); }
 
-template <int WM, int WN, int FM, int FN, int NS, bool GROUPED, int KG = 1>
+template <int WM, int WN, int FM, int FN, int NS, bool GROUPED, int KS = 1, int KG = 1>
 hipError_t tile_launch(ProductParams p, hipStream_t st) {
-  using T = Tile<WM, WN, FM, FN, NS, KG>;
+  using T = Tile<WM, WN, FM, FN, NS, KS, KG>;
   const int ntiles = column_tiles(p, T::BN);
   const int64_t resident = int64_t(std::max(xcd_compute_units(), 1)) * kXcds * T::groups(GROUPED);
   const int32_t all = GROUPED ? p.blocks : int32_t((p.M + T::BM - 1) / T::BM);
@@ -750,7 +745,7 @@ hipError_t tile_launch(ProductParams p, hipStream_t st) {
   for (p.block0 = 0; p.block0 < all; p.block0 += most) {
     p.blocks = std::min(most, all - p.block0);
     const int64_t grid = std::min(int64_t(p.blocks) * ntiles, resident);
-    hipLaunchKernelGGL((gemm_tile_kernel<WM, WN, FM, FN, NS, GROUPED, KG>), dim3(unsigned(grid)),
+    hipLaunchKernelGGL((gemm_tile_kernel<WM, WN, FM, FN, NS, GROUPED, KS, KG>), dim3(unsigned(grid)),
                        dim3(T::NW * kWave), 0, st, p, ntiles);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -787,41 +782,65 @@ hipError_t rows_of(const ProductParams& p, hipStream_t st) {
 
 }  // namespace
 
+// Estimates in microseconds, fitted to measured shapes with W from memory.  A tile
+// takes `block` for each 64 of K and each round over the device (one workgroup a
+// CU; with fewer tiles than CUs up to a fifth less), `once` a round and `base` a
+// call.  Few rows straight from memory: a wavefront's latency over K, for each
+// round.
+//
+// Measured: rows, 32 x 32, 64 x 64, 32 x 128 and 64 x 128: 1 row of 2880 x 2880 5.7,
+// 8.5, 11.8, 13.5 and 13.3; 16 rows of 4096 x 4096 9.7, 10.1, 15.2, 17.4 and 17.2; 64 -,
+// 10.5, 16.7, 18.0 and 21.6; 256 -, 32.5, 17.5, 19.8 and 21.8; 333 of 2880 x 2880 -, 30,
+// 25.6, 16.4 and 18.7.  64 x 128, 128 x 128, 128 x 256 and 256 x 256: 512 of 4096 x 4096
+// 26, 30, 45 and 74; 1024 46, 37, 45 and 75; 2048 89, 69, 59 and 76; 4000 of 512 x 4096
+// 33, 26, 23 and 21; 4096 of 4096 x 12288 -, -, 333 and 289.
 hipError_t launch_gemm(ProductParams p, hipStream_t st) {
   const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
-  auto rounds = [&](int bm, int bn, int64_t at_once) {
-    const int64_t tiles = (p.M + bm - 1) / bm * column_tiles(p, bn);
-    return (tiles + at_once - 1) / at_once;
+  struct Shape {
+    int rows, cols;
+    double block, once, base;
   };
-  const bool once32 = rounds(32, 32, cus) == 1, once64 = rounds(64, 64, cus) == 1;
-  const int64_t cost[5] = {once64 ? 30 : 50 * rounds(64, 64, 2 * cus), 43 * rounds(64, 128, cus),
-                           63 * rounds(128, 128, cus), 98 * rounds(128, 256, cus),
-                           175 * rounds(256, 256, cus)};
-  const int best = int(std::min_element(cost, cost + 5) - cost);
-  const int64_t groups = (p.N + 15) / 16, passes = (p.M + 31) / 32;
-  const double mb = 2e-6 * p.N * p.K;
-  const double by_rows = 1.8 + 1e-3 * p.K + std::max(mb * (p.M <= 16 ? 0.18 : 0.3 * double(passes)),
-                                                     (p.M <= 16 ? 8e-4 : 1.6e-3) * double(groups * passes));
-  const double by_32 = once32 ? 3.5 + 2.8e-3 * p.K : INFINITY;
-  const double by_tile = 3 + 0.01 * p.KB * double(cost[best]);
-  const bool wide = p.gated || groups > cus;
-  const int64_t grid = p.M > 16 ? (p.gated ? rows_grid<2, 2, false>(p) : rows_grid<2, 1, false>(p))
-                       : wide   ? rows_grid<1, 2, false>(p)
-                                : rows_grid<1, 1, false>(p);
-  if (by_rows < std::min(by_32, by_tile) && rows_fit(grid)) {
-    if (p.M > 16) return p.gated ? rows_of<2, 2, false>(p, st) : rows_of<2, 1, false>(p, st);
-    return wide ? rows_of<1, 2, false>(p, st) : rows_of<1, 1, false>(p, st);
+  constexpr Shape shapes[] = {{32, 32, 0.1, 0, 3.8},    {32, 128, 0.27, 0, 2.5},  {64, 64, 0.222, 0, 2.5},
+                              {64, 128, 0.34, 0, 2.5},  {128, 128, 0.53, 0, 3.0}, {128, 256, 0.85, 1.5, 3.0},
+                              {256, 256, 1.45, 3.0, 4.0}};
+  int best = 0;
+  double least = INFINITY;
+  for (int i = 0; i < 7; ++i) {
+    const Shape& s = shapes[i];
+    const int64_t tiles = (p.M + s.rows - 1) / s.rows * column_tiles(p, s.cols);
+    const double rounds = double((tiles + cus - 1) / cus), part = std::min(1.0, double(tiles) / double(cus));
+    const double cost = s.base + rounds * (s.block * p.KB * (0.8 + 0.2 * part) + s.once);
+    if (cost < least) least = cost, best = i;
   }
-  if (by_32 < by_tile) return tile_launch<1, 1, 2, 2, 3, false, 4>(p, st);
+  if (p.M <= 16) {
+    // (gated, gate and up of 16 columns)
+    const int64_t grid = p.gated ? rows_grid<1, 2, false>(p) : rows_grid<1, 1, false>(p);
+    const double rounds = double((grid + cus - 1) / cus);
+    const double by_rows = p.gated ? 2.0 + 2.9e-3 * p.K * rounds : 1.0 + 1.8e-3 * p.K * rounds;
+    if (by_rows < least && rows_fit(grid))
+      return p.gated ? rows_of<1, 2, false>(p, st) : rows_of<1, 1, false>(p, st);
+  }
   switch (best) {
-    case 0: return tile_launch<2, 2, 2, 2, 4, false>(p, st);
-    case 1: return tile_launch<2, 4, 2, 2, 4, false>(p, st);
-    case 2: return tile_launch<2, 4, 4, 2, 2, false>(p, st);
-    case 3: return tile_launch<2, 4, 4, 4, 2, false>(p, st);
+    case 0: return tile_launch<1, 1, 2, 2, 3, false, 1, 4>(p, st);
+    case 1: return tile_launch<1, 4, 2, 2, 3, false, 2>(p, st);
+    case 2: return tile_launch<2, 2, 2, 2, 3, false, 2>(p, st);
+    case 3: return tile_launch<2, 4, 2, 2, 3, false, 2>(p, st);
+    case 4: return tile_launch<2, 4, 4, 2, 4, false>(p, st);
+    case 5: return tile_launch<2, 4, 4, 4, 3, false>(p, st);
     default: return tile_launch<2, 4, 8, 4, 2, false>(p, st);
   }
 }
 
+// Estimates in microseconds, with the pairs spread evenly: `stream`, one expert's
+// weights at 5.5 TB/s.  The rows kernel takes 3 us, and for each piece of 16 rows
+// those weights or 4 ns a workgroup; the tiles take 10 us, of which most is
+// finding them, and each expert's weights once, or, with few of them, the
+// latency of their K.  Measured, rows and tiles: 8 experts of 512 x 1024, 8 rows each,
+// 5.7 and 13.5, 96 rows 12.3 and 15.8; 8 of 2048 x 4096, 8 rows 30 and 54, 48 rows 75
+// and 59; 128 of 2880 x 2880, 8 rows 361 and 363, 16 rows 477 and 370; 64 of 1536 x
+// 1024, 4 rows 38 and 45.  Routing that leaves most pairs to few experts is not
+// seen: the rows kernel then reads their weights once for every 16 rows, whatever
+// the tiles would take.
 hipError_t launch_moe_gemm(ProductParams p, hipStream_t st) {
   const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
   const int64_t E = p.E, used = std::min<int64_t>(p.numel, E);
@@ -832,14 +851,24 @@ hipError_t launch_moe_gemm(ProductParams p, hipStream_t st) {
   const double by_rows = 3 + double(tiles(16)) * std::max(stream, 0.004 * groups);
   const double by_tiles = 10 + std::max(0.45 * p.KB, 0.2 * p.KB + double(used) * stream);
   if (by_rows <= by_tiles && rows_fit(rows_grid<1, 2, true>(p))) {
-    if (p.numel >= 3 * E && used * column_tiles(p, 64) >= cus) return rows_of<1, 4, true>(p, st);
+    // 64 columns a workgroup read X half as often as 32, where that leaves a
+    // workgroup for every CU (32 experts of 5760 x 2880, 2 rows each, 167.5 us and
+    // 171; 8 of 512 x 1024, 96 rows 12.3 and 14.9, 8 rows 7.6 and 5.8)
+    if (tiles(16) * column_tiles(p, 64) >= cus) return rows_of<1, 4, true>(p, st);
     return rows_of<1, 2, true>(p, st);
   }
+  // The tile whose rounds over the device cost least, the largest only with enough
+  // rows to fill it whatever the routing.  (64 x 256, 128 x 256 and 256 x 256) 128
+  // experts of 1536 x 2048: 32 rows each 155, 155 and 157 us, 64 rows 191, 175 and
+  // 180, 128 rows 233, 205 and 196, 512 rows 606, 462 and 437; of 2880 x 2880, 128
+  // rows 656, 547 and 483; 16 of 2048 x 4096: 96 rows 73, 80 and 87, 192 rows 115, 79
+  // and 99, 256 rows 157, 125 and 102; skewed routing over 64 of 1024 x 1024, 96 rows:
+  // 51, 45 and 57; 8 of 512 x 512, 300 rows: 12, 15 and 20.
   const int64_t cols = column_tiles(p, 256);
   auto rounds = [&](int rows) { return (tiles(rows) * cols + cus - 1) / cus; };
   const int64_t cost64 = 80 * rounds(64), cost128 = 98 * rounds(128), cost256 = 140 * rounds(256);
   if (p.block_m <= 64 && cost64 <= cost128) return tile_launch<2, 4, 2, 4, 3, true>(p, st);
-  if (p.numel <= 96 * E || cost128 <= cost256) return tile_launch<2, 4, 4, 4, 2, true>(p, st);
+  if (p.numel <= 96 * E || cost128 <= cost256) return tile_launch<2, 4, 4, 4, 3, true>(p, st);
   return tile_launch<2, 4, 8, 4, 2, true>(p, st);
 }
 
