@@ -274,7 +274,8 @@ __device__ __forceinline__ bool pick(const RouteParams& p, uint32_t (&key)[V], u
   }
   if constexpr (kCheck) {
     if (r == topk) beyond = wave_max(key[0]);
-    const T next = lane == first + topk - 1 ? beyond : __shfl_down(mine, 1);
+    // (every lane takes part in the exchange, the last pick's too)
+    const T below = __shfl_down(mine, 1), next = lane == first + topk - 1 ? beyond : below;
     return __ballot(uint32_t(lane - first) < uint32_t(topk) && open_between(value_of(mine), value_of(next), p.sigmoid));
   }
   return false;
