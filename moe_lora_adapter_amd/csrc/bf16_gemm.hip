@@ -220,9 +220,12 @@ __device__ __forceinline__ void finish_tile(const ProductParams& p, f32x4_t (&ac
 // ---------------------------------------------------------------- few rows
 // One workgroup computes 16 MT rows x 16 NT columns of W: its kSplit wavefronts
 // take the stages w, w + kSplit, ... of K straight from memory and add their sums
-// in LDS, in order.  Gated, the even groups of 16 columns are gate's and the odd
-// ones the same of up.  Grouped, the workgroups of a block take its pieces of 16
-// rows in steps of `step` rows.
+// in LDS, in order.  Bound by the stream of W: 20b-like decode w13 (64 pairs, 940
+// MB) 167 us, 5.6 TB/s, 120b-like decode w2 79 us, 6.0; more stages in flight a
+// wavefront are slower there (two 184 us) and no faster where a CU has one
+// workgroup (1 row of 4096 x 4096: 8.4 us, two 9.9, four 9.3).  Gated, the even
+// groups of 16 columns are gate's and the odd ones the same of up.  Grouped, the
+// workgroups of a block take its pieces of 16 rows in steps of `step` rows.
 constexpr int kSplit = 8;
 template <int MT, int NT, bool GROUPED>
 __global__ void __launch_bounds__(kSplit * kWave) gemm_rows_kernel(ProductParams p, int ntiles, uint32_t step) {
@@ -377,8 +380,16 @@ __global__ void __launch_bounds__(kSplit * kWave) gemm_rows_kernel(ProductParams
 // stages of one are multiplied while the first of the next are on their way,
 // and its results are stored in that time too.
 //
-// KG > 1, for small tiles: a stage has KG blocks of 64, each of which WM x WN
-// wavefronts multiply, and their sums meet in LDS.
+// Large products are bound by the card's power and by this loop: 4096 x 4096 x
+// 12288 takes 289 to 300 us (1.37 to 1.43 PFLOP/s), the matrix cores 68 % busy at
+// 1.94 GHz.  Matrix instructions alone, on random operands in registers, reach 1.97
+// PFLOP/s at 2.1 GHz; this loop without its loads, on zeros, takes 217 us at 2.45
+// GHz.  No LDS bank conflicts.  A 128 x 64 tile a wavefront reads 192 KB of LDS a
+// stage; 128 x 128 with four wavefronts reads 128 KB and was no faster.
+//
+// KS > 1: a stage has KS blocks of 64, which share its barrier.  KG > 1, for few
+// tiles: KG groups of WM x WN wavefronts multiply a block each, and their sums meet
+// in LDS.
 template <int WM, int WN, int FM, int FN, int NS, int KS = 1, int KG = 1>
 struct Tile {
   static constexpr int BM = WM * FM * 16, BN = WN * FN * 16, NW = WM * WN * KG;

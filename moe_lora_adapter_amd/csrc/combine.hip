@@ -3,7 +3,9 @@
 // is not read (its row of y was never written).
 //
 // Memory-bound: each value is read once, 16 bytes a lane, the loads of kAtOnce
-// pairs in flight before the first is used.
+// pairs in flight before the first is used.  8192 tokens x 8 x 2048 columns 60 us,
+// 5.4 TB/s (a copy reaches 5.2); 16 x 4 x 2880 2.5 us in a graph, launch and one
+// round trip.
 #include <algorithm>
 
 #include "base.h"

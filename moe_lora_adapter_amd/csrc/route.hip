@@ -7,8 +7,12 @@
 //
 // One wavefront a row, V consecutive experts a lane, each lane's sorted, so that a
 // pick is one maximum over the lanes' first keys and one lane's step to its next,
-// and ties fall to the lowest lane.  Bound by those instructions (some 25 a pick,
-// 10 a score).
+// and ties fall to the lowest lane.  Bound by those instructions: 65536 rows of 256
+// experts in 8 groups 75 us, 480 vector instructions a row (some 22 a pick, 10 a
+// score, 60 the groups), the vector units two thirds busy; without groups 61, by
+// logits 36, one pick by logits 21 (3.2 TB/s).  8192 x 128 by logits 6.9 us.  A lane
+// with every 64th expert instead of V in a row, picks by comparisons of floats and
+// weights row by row took 110.
 //
 // Which of two nearly equal scores is larger must not hang on a rounding: keys
 // are computed in fp32, and a row where two keys that decide something are closer
