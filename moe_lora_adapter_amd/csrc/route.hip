@@ -163,8 +163,13 @@ __device__ __forceinline__ auto group_score(const RouteParams& p, T a, T b, int 
     a = c > a ? c : a;
     b = low > high ? low : high;
   }
-  const auto s = value_of(a);
-  return p.group_top == 2 && b > none<T>() ? s + value_of(b) : s;
+  auto s = value_of(a);
+  if (p.group_top == 2 && b > none<T>()) {
+    s += value_of(b);
+    // a sum below fp32's range is no empty group's: two of them are left to fp64
+    if constexpr (sizeof(T) == 4) s = fmaxf(s, -3.4028234663852886e38f);
+  }
+  return s;
 }
 
 // What another lane of this wavefront wrote to LDS before is read behind this.

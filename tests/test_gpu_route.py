@@ -152,6 +152,26 @@ def test_scores_decide_as_in_fp64():
         both(y[None], 8, scoring="sigmoid", **kw)
 
 
+@pytest.mark.parametrize("E,G", [(16, 4), (24, 4), (256, 8), (512, 16), (96, 4)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_whose_sums_leave_fp32(E, G, scoring):
+    """Biases of the type's lowest and largest values: two of them are beyond fp32, and such a group is
+    still one with experts, ahead of the empty ones around it and in its place among the others."""
+    n, big = E // G, torch.finfo(torch.float32).max
+    kw = dict(scoring=scoring, n_group=G, group_top=2)
+    x = torch.randn((8, E), generator=gen(E))
+    x[:, :n] = x[:, 4 * n:] = NEG
+    b = torch.zeros(E)
+    b[n:3 * n] = -big
+    both(x, min(3 * n, 64), b, topk_group=3, **kw)
+    both(x, 2 * n, b, topk_group=2, **kw)  # groups 3 and 1
+    b[2 * n + 1:3 * n] = -big / 2  # two of them are in range: groups 3 and 2
+    both(x, 2 * n, b, topk_group=2, **kw)
+    b[n:2 * n], b[2 * n:3 * n] = big / 1.5, big  # groups 2 and 1
+    both(x, 2 * n, b, topk_group=2, **kw)
+    both(x, 2, b, topk_group=1, **kw)
+
+
 def test_weights_of_far_picks_do_not_underflow():
     """Picks that a bias chose far below the row's largest logit are renormalised among themselves."""
     x = torch.zeros((2, 16))
