@@ -8,16 +8,19 @@
 // One wavefront a row, V consecutive experts a lane, each lane's sorted, so that a
 // pick is one maximum over the lanes' first keys and one lane's step to its next,
 // and ties fall to the lowest lane.  Bound by those instructions: 65536 rows of 256
-// experts in 8 groups 75 us, 480 vector instructions a row (some 22 a pick, 10 a
-// score, 60 the groups), the vector units two thirds busy; without groups 61, by
-// logits 36, one pick by logits 21 (3.2 TB/s).  8192 x 128 by logits 6.9 us.  A lane
+// experts in 8 groups 69 us, 480 vector instructions a row (some 22 a pick, 10 a
+// score, 60 the groups), the vector units 71 % busy; without groups 56, by logits 36, one
+// pick by logits 21 (3.2 TB/s).  8192 x 128 by logits 6.9 us.  A lane
 // with every 64th expert instead of V in a row, picks by comparisons of floats and
 // weights row by row took 110.
 //
 // Which of two nearly equal scores is larger must not hang on a rounding: keys
 // are computed in fp32, and a row where two keys that decide something are closer
-// than fp32's error is done again in fp64 by the same wavefront.  Keys that are x
-// itself are exact.
+// than fp32's error is done again in fp64 by the same wavefront, when it has been
+// through all its rows: at once, both passes' registers together leave four
+// wavefronts a SIMD and not six (65536 x 256 in 8 groups 76 us and 69, 32768 x 64 23
+// and 24).  Until then such a row's first id is kOpen.  Keys that are x itself are
+// exact.
 #include <algorithm>
 
 #include "base.h"
@@ -28,6 +31,7 @@ namespace mlr {
 namespace {
 
 constexpr int kWaves = 4;  // of a workgroup, a row each
+constexpr int32_t kOpen = INT32_MIN;
 
 // ---------------------------------------------------------------- keys
 // fp32 keys are compared as unsigned integers in the same order, so that a step of
@@ -376,6 +380,17 @@ __device__ __forceinline__ bool pick_row(const RouteParams& p, const float (&x)[
   }
   // the largest logit, where scores are relative to it
   const float m = !p.sigmoid && (BY_SCORE || !p.renorm) ? value_of(wave_max(top)) : 0.0f;
+  if (!p.sigmoid && !p.renorm) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      sum += x[j] > kMasked ? exact_exp_from(x[j], m) : 0.0f;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    sum = sum_over(sum, kWave);
+    out->m = mine ? m : out->m;
+    out->sum = mine ? sum : out->sum;
+  }
   if constexpr (BY_SCORE) {
     uint32_t key[V];
     nan |= score_keys(p, x, bias, m, key);
@@ -388,26 +403,15 @@ __device__ __forceinline__ bool pick_row(const RouteParams& p, const float (&x)[
   }
   const bool bad = __ballot(nan) != 0;
   out->nan = mine ? bad : out->nan;
-  if (!p.sigmoid && !p.renorm) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      sum += x[j] > kMasked ? exact_exp_from(x[j], m) : 0.0f;
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    sum = sum_over(sum, kWave);
-    out->m = mine ? m : out->m;
-    out->sum = mine ? sum : out->sum;
-  }
   return open;
 }
 
-// The same picks in fp64.  Few rows come here: an expert at a time, the keys in
-// LDS, so that it takes no more registers than the rest.
+// The same picks in fp64, into the first lanes.  Few rows come here: an expert at a
+// time, the keys in LDS, so that it takes few registers.
 template <typename X>
-__device__ __forceinline__ void pick_again(const RouteParams& p, const X* row, double* lds, int first, bool mine,
-                                           Lane* out) {
+__device__ __forceinline__ Lane pick_again(const RouteParams& p, const X* row, double* lds) {
   const int lane = lane_id();
+  bool nan = false;
   auto logit = [&](int e) {
     if constexpr (sizeof(X) == 4)
       return row[e];
@@ -423,6 +427,7 @@ __device__ __forceinline__ void pick_again(const RouteParams& p, const X* row, d
   for (int e = lane; e < p.E; e += kWave) {
     const float x = logit(e);
     const double s = p.sigmoid ? 1.0 / (1.0 + exp(-double(x))) : exp_from(double(x), m);
+    nan |= x != x;
     lds[e] = x > kMasked ? s : none<double>();
     sum += x > kMasked ? s : 0.0;
   }
@@ -430,7 +435,9 @@ __device__ __forceinline__ void pick_again(const RouteParams& p, const X* row, d
 #pragma unroll 1
   for (int e = lane; e < p.E; e += kWave) {
     const double s = lds[e];
-    lds[e] = s > none<double>() ? key_of<double>(s / sum + (p.bias ? double(p.bias[e]) : 0.0)) : s;
+    const double key = s / sum + (p.bias ? double(p.bias[e]) : 0.0);
+    nan |= s > none<double>() && key != key;
+    lds[e] = s > none<double>() ? key_of<double>(key) : s;
   }
   wave_sync();
   if (p.n_group > 1) {
@@ -443,7 +450,7 @@ __device__ __forceinline__ void pick_again(const RouteParams& p, const X* row, d
       if (!(kept >> (uint32_t(e) * p.inv_size >> 20 << shift) & 1)) lds[e] = none<double>();
     wave_sync();
   }
-  out->id = mine ? -1 : out->id;
+  Lane out{-1, float(m), float(sum), __ballot(nan) != 0};
   for (int r = 0; r < p.topk; ++r) {
     double best = none<double>();
     uint32_t at = 0;
@@ -456,17 +463,20 @@ __device__ __forceinline__ void pick_again(const RouteParams& p, const X* row, d
     const double most = wave_max(best);
     if (!(most > none<double>())) break;
     const int e = int(~wave_max(best == most ? ~at : 0u));  // the lowest of equal ones
-    out->id = lane == first + r ? e : out->id;
+    out.id = lane == r ? e : out.id;
     if (lane == 0) lds[e] = none<double>();
     wave_sync();
   }
+  return out;
 }
 
-// The weights of `rows` rows, a pick a lane, 2^each lanes a row.
+// The weights of `rows` rows, a pick a lane, 2^each lanes a row; `open` has the rows
+// to be done again.
 // Renormalised, the common factor cancels, and everything is relative to the
 // largest of the row's picks, so that none underflows.
 template <typename X>
-__device__ __forceinline__ void weigh_rows(const RouteParams& p, int64_t row0, int rows, int each, const Lane& in) {
+__device__ __forceinline__ void weigh_rows(const RouteParams& p, int64_t row0, int rows, int each, const Lane& in,
+                                           uint64_t open) {
   const int lane = lane_id(), q = lane >> each, r = lane & ((1 << each) - 1);
   const int64_t row = row0 + q;
   const bool have = in.id >= 0;
@@ -501,7 +511,7 @@ __device__ __forceinline__ void weigh_rows(const RouteParams& p, int64_t row0, i
   s *= p.scale;
   if (in.nan) s = __builtin_nanf("");
   if (r < p.topk && q < rows) {
-    p.ids[row * p.topk + r] = in.id;
+    p.ids[row * p.topk + r] = r == 0 && (open >> q & 1) ? kOpen : in.id;
     p.weights[row * p.topk + r] = s;
   }
 }
@@ -514,8 +524,10 @@ __global__ void __launch_bounds__(kWaves * kWave) route_kernel(RouteParams p) {
   const int lane = lane_id(), w = wave_id(), each = p.slot_shift;
   const X* logits = reinterpret_cast<const X*>(p.logits);
   const int64_t step = int64_t(gridDim.x) * kWaves * p.batch;
-  int64_t row0 = (int64_t(blockIdx.x) * kWaves + w) * p.batch;
+  const int64_t first = (int64_t(blockIdx.x) * kWaves + w) * p.batch;
+  int64_t row0 = first;
   if (row0 >= p.M) return;
+  bool any = false;
   float bias[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) bias[j] = BY_SCORE && p.bias ? p.bias[min(V * lane + j, p.E - 1)] : 0.0f;
@@ -534,13 +546,18 @@ __global__ void __launch_bounds__(kWaves * kWave) route_kernel(RouteParams p) {
 #pragma unroll
       for (int j = 0; j < V; ++j) x[j] = next[j];
     }
-    if constexpr (BY_SCORE) {
-      for (; open; open &= open - 1) {
-        const int q = __builtin_ctzll(open);
-        pick_again(p, logits + (row0 + q) * p.E, lds[w], q << each, lane >> each == q, &out);
-      }
+    weigh_rows<X>(p, row0, rows, each, out, open);
+    any |= open != 0;
+  }
+  if (!BY_SCORE || !any) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // another lane wrote the id
+  for (row0 = first; row0 < p.M; row0 += step) {
+    const int rows = int(std::min<int64_t>(p.batch, p.M - row0));
+    uint64_t open = __ballot(lane < rows && p.ids[(row0 + std::min(lane, rows - 1)) * p.topk] == kOpen);
+    for (; open; open &= open - 1) {
+      const int64_t row = row0 + __builtin_ctzll(open);
+      weigh_rows<X>(p, row, 1, each, pick_again(p, logits + row * p.E, lds[w]), 0);
     }
-    weigh_rows<X>(p, row0, rows, each, out);
   }
 }
 

@@ -122,3 +122,19 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("E", [8, 256])
+def test_every_row_undecided(E):
+    """More rows than the wavefronts take at once, all with equal scores: fp32 decides none of them."""
+    M, topk = (2_500_000, 4) if E == 8 else (1_200_000, 8)
+    g = torch.Generator(device=DEV).manual_seed(E)
+    x = torch.randint(0, 2, (M, E), generator=g, device=DEV).to(torch.bfloat16)
+    ids, w = mla.moe_lora_route(x, topk, scoring="sigmoid", bias=torch.zeros(E, device=DEV))
+    # the ones first, each kind in ascending order
+    at = torch.arange(E, device=DEV)
+    want = torch.topk((1 - x.long()) * E + at, topk, dim=1, largest=False, sorted=True).values
+    assert torch.equal(ids.long(), want % E)
+    s = torch.sigmoid((want < E).double())
+    # (the exponential, two quotients and up to 8 additions: below 32 half steps)
+    assert torch.allclose(w.double(), s / s.sum(1, keepdim=True), rtol=2 ** -19, atol=0)
