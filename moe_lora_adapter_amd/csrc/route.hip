@@ -37,6 +37,7 @@ constexpr int32_t kOpen = INT32_MIN;
 // fp32 keys are compared as unsigned integers in the same order, so that a step of
 // a maximum over lanes is one instruction; fp64 ones as they are.
 constexpr float kMasked = -__builtin_huge_valf();
+constexpr float kMost = 3.4028234663852886e38f;
 
 template <typename T>
 constexpr T none();  // below every key: masked, or picked already
@@ -127,22 +128,33 @@ __device__ __forceinline__ T exp_from(T x, T m) {
 }
 __device__ __forceinline__ float exact_exp_from(float x, float m) { return x == m ? 1.0f : expf(x - m); }
 
-// Whether fp32 leaves open which of two keys, or groups' sums of two, a >= b is
-// larger.  A sigmoid is off by less than 2^-22: s (1 - s) times the exponential's
-// error (1.5 |x| 2^-24 for its argument, 2^-23 its own; |x| s (1 - s) < 1/4), the
-// addition's 2^-24 and the reciprocal's 2^-23.  A softmax's share is off by less than
-// 2^-18: up to 21 additions and the exponentials' errors (|d| < 8 on average) in the
-// sum.  The bias and a group's sum add roundings of the key.
+// Whether fp32 leaves open which of two keys a >= b is larger.  A sigmoid is off by
+// less than 2^-22: s (1 - s) times the exponential's error (1.5 |x| 2^-24 for its
+// argument, 2^-23 its own; |x| s (1 - s) < 1/4), the addition's 2^-24 and the
+// reciprocal's 2^-23.  A softmax's share is off by less than 2^-18: up to 21 additions
+// and the exponentials' errors (|d| < 8 on average) in the sum.  The bias adds a
+// rounding of the key.
 __device__ __forceinline__ bool open_between(float a, float b, int sigmoid) {
   return b > kMasked && !(a - b > (sigmoid ? 0x1p-20f : 0x1p-16f) + 0x1p-21f * fmaxf(fabsf(a), fabsf(b)));
 }
-__device__ __forceinline__ bool open_between(double, double, int) { return false; }
 
 // ---------------------------------------------------------------- picking
-// Groups' ranks from their scores, the same in all `lanes` lanes of a group.
-// Returns whether fp32 leaves the cut open.
+// A group's score, and the size of the keys in it: what their roundings go by, where
+// two of opposite signs leave a small sum.
 template <typename F>
-__device__ __forceinline__ bool rank_groups(const RouteParams& p, F score, int group, int lanes, int* rank) {
+struct GroupScore {
+  F sum, size;
+};
+
+// Groups' ranks from their scores, the same in all `lanes` lanes of a group.
+// Returns whether fp32 leaves the cut open: whether some group's score is nearer to
+// the middle of the two next to the cut than it may be off, two keys' scores (see
+// open_between) and three roundings of at most its size.  All are looked at, not
+// those two alone: one group's keys may be far larger than the others'.
+template <typename F>
+__device__ __forceinline__ bool rank_groups(const RouteParams& p, const GroupScore<F>& of, int group, int lanes,
+                                            int* rank) {
+  const F score = of.sum;
   int r = 0;
   for (int g = 0; g < p.n_group; ++g) {
     const F v = from_lane(score, g * lanes);
@@ -152,13 +164,20 @@ __device__ __forceinline__ bool rank_groups(const RouteParams& p, F score, int g
   if (p.topk_group == p.n_group) return false;
   const uint64_t in = __ballot(group < p.n_group && r == p.topk_group - 1);
   const uint64_t next = __ballot(group < p.n_group && r == p.topk_group);
-  return open_between(from_lane(score, __builtin_ctzll(in)), from_lane(score, __builtin_ctzll(next)), p.sigmoid);
+  if constexpr (sizeof(F) == 4) {
+    const float low = from_lane(score, __builtin_ctzll(next));
+    if (!(low > kMasked)) return false;  // behind the cut all are empty
+    const float cut = 0.5f * from_lane(score, __builtin_ctzll(in)) + 0.5f * low;
+    const bool sure = fabsf(score - cut) > fmaf(0x1p-22f, of.size, p.sigmoid ? 0x1p-21f : 0x1p-17f);
+    return __ballot(group < p.n_group && !sure) != 0;
+  }
+  return false;
 }
 
 // The best two of all keys of this lane's group, from those of a lane, a >= b; the
 // group's score.
 template <typename T>
-__device__ __forceinline__ auto group_score(const RouteParams& p, T a, T b, int lanes) {
+__device__ __forceinline__ GroupScore<decltype(value_of(T()))> group_score(const RouteParams& p, T a, T b, int lanes) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     if (o >= lanes) continue;
@@ -167,13 +186,15 @@ __device__ __forceinline__ auto group_score(const RouteParams& p, T a, T b, int 
     a = c > a ? c : a;
     b = low > high ? low : high;
   }
-  auto s = value_of(a);
+  auto s = value_of(a), size = s;
+  if constexpr (sizeof(T) == 4) size = fabsf(s);
   if (p.group_top == 2 && b > none<T>()) {
     s += value_of(b);
     // a sum below fp32's range is no empty group's: two of them are left to fp64
-    if constexpr (sizeof(T) == 4) s = fmaxf(s, -3.4028234663852886e38f);
+    if constexpr (sizeof(T) == 4) s = fmaxf(s, -kMost), size += fabsf(value_of(b));
   }
-  return s;
+  if constexpr (sizeof(T) == 4) size = fminf(size, kMost);  // (an empty group's is far from any cut)
+  return {s, size};
 }
 
 // What another lane of this wavefront wrote to LDS before is read behind this.
