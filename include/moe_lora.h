@@ -648,6 +648,20 @@ MOE_LORA_API int moe_lora_moe_gemm(const uint16_t *x, int32_t x_per_pair, const 
                    void *stream);
 
 /*
+ * moe_lora_gemm_kernel_name, moe_lora_moe_gemm_kernel_name -- [host, nothing
+ * launched] the kernel that moe_lora_gemm and moe_lora_moe_gemm launch for these
+ * sizes on the current device (for an MI355X's 256 compute units where there is
+ * none), and its rows x columns of w: "gemm_rows_kernel 16x16" (few rows) or
+ * "gemm_tile_kernel 256x256", the larger ones with some of both.  A static
+ * string; NULL for sizes that the call refuses and for M == 0.
+ */
+MOE_LORA_API const char *moe_lora_gemm_kernel_name(int64_t M, int32_t K, int32_t Ns, int32_t S,
+                   int32_t activation);
+MOE_LORA_API const char *moe_lora_moe_gemm_kernel_name(int64_t M, int32_t topk, int32_t K,
+                   int32_t Ns, int32_t S, int32_t E, int32_t block_m, int32_t x_per_pair,
+                   int32_t activation);
+
+/*
  * moe_lora_combine -- out[m, :] = bf16( sum_k w[m, k] * y[m, k, :] + residual[m, :] ):
  * a token's expert outputs joined, in ascending k, in fp32, rounded once.  w is 1
  * when topk_weights is NULL (the product has applied them).  With topk_ids, pairs

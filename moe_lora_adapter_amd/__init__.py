@@ -86,6 +86,9 @@ SIGNATURES = {
                                      _P]),
     "moe_lora_moe_gemm": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I64, _I32,
                                          _I32, _I32, _I32, _I32, _I32, _I32, _P, _P]),
+    "moe_lora_gemm_kernel_name": (ctypes.c_char_p, [_I64, _I32, _I32, _I32, _I32]),
+    "moe_lora_moe_gemm_kernel_name": (ctypes.c_char_p, [_I64, _I32, _I32, _I32, _I32, _I32, _I32,
+                                                        _I32, _I32]),
     "moe_lora_combine": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I64, _I32, _I32, _P, _P]),
 }
 
@@ -850,6 +853,24 @@ def moe_lora_moe_gemm(x, w, align: AlignOutput, topk_weights, y, *, mul_routed_w
     if rc != OK:
         raise MoeLoraError(rc, "moe_lora_moe_gemm")
     return y
+
+
+def gemm_kernel_name(M: int, K: int, Ns: int, S: int, activation: str | None = None) -> str:
+    """Name and tile of the GPU kernel moe_lora_gemm launches for these sizes."""
+    name = lib().moe_lora_gemm_kernel_name(M, K, Ns, S, _activation(activation)[0])
+    if name is None:
+        raise MoeLoraError(ERR_INVALID, "moe_lora_gemm_kernel_name")
+    return name.decode()
+
+
+def moe_gemm_kernel_name(M: int, topk: int, K: int, Ns: int, S: int, E: int, block_m: int,
+                         x_per_pair: bool = False, activation: str | None = None) -> str:
+    """Name and tile of the GPU kernel moe_lora_moe_gemm launches for these sizes."""
+    name = lib().moe_lora_moe_gemm_kernel_name(M, topk, K, Ns, S, E, block_m,
+                                               int(bool(x_per_pair)), _activation(activation)[0])
+    if name is None:
+        raise MoeLoraError(ERR_INVALID, "moe_lora_moe_gemm_kernel_name")
+    return name.decode()
 
 
 def moe_lora_combine(y, out=None, *, topk_weights=None, topk_ids=None, E: int | None = None,

@@ -36,6 +36,39 @@ int check_product(int64_t K, int64_t Ns, int64_t S, int32_t act, ProductParams* 
 // Workgroups of a launch: 16 rows x 16 columns is the smallest tile.
 bool grid_fits(int64_t blocks, int64_t N) { return blocks <= kInt32Max / ((N + 15) / 16); }
 
+// All sizes of a dense product.
+int check_dense(int64_t M, int64_t K, int64_t Ns, int64_t S, int32_t act, ProductParams* p) {
+  if (M < 0) return MOE_LORA_ERR_INVALID;
+  const int rc = check_product(K, Ns, S, act, p);
+  if (rc != MOE_LORA_OK) return rc;
+  if (M > kInt32Max || !grid_fits((M + 15) / 16, p->N)) return MOE_LORA_ERR_UNSUPPORTED;
+  p->rows = p->M = M;
+  return MOE_LORA_OK;
+}
+
+// And of a grouped one.
+int check_grouped(int64_t M, int32_t topk, int64_t K, int64_t Ns, int64_t S, int32_t E, int32_t block_m,
+                  int32_t x_per_pair, int32_t act, ProductParams* p) {
+  // the align step's own limits on M, topk, E and block_m, for one slot
+  const int64_t cap = moe_lora_align_capacity(M, topk, E, block_m);
+  if (cap < 0) return int(cap);
+  const int rc = check_product(K, Ns, S, act, p);
+  if (rc != MOE_LORA_OK) return rc;
+  if (!flag(x_per_pair)) return MOE_LORA_ERR_INVALID;
+  const int64_t numel = M * topk, rows = x_per_pair ? numel : M;
+  const int64_t blocks = max_total_blocks(numel, E, block_m);
+  if (rows > kMaxElements / K || !grid_fits(blocks * (block_m / 16), p->N)) return MOE_LORA_ERR_UNSUPPORTED;
+  p->rows = rows;
+  p->M = M;
+  p->numel = int32_t(numel);
+  p->topk = topk;
+  p->E = E;
+  p->block_m = block_m;
+  p->x_per_pair = x_per_pair;
+  p->blocks = int32_t(blocks);
+  return MOE_LORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -83,10 +116,9 @@ int moe_lora_gemm(const uint16_t* x, const uint16_t* w, const uint16_t* bias, co
                   const uint16_t* residual, int64_t M, int32_t K, int32_t Ns, int32_t S,
                   int32_t activation, int32_t y_fp32, void* y, void* stream) {
   ProductParams p{};
-  if (M < 0 || !flag(y_fp32)) return MOE_LORA_ERR_INVALID;
-  const int rc = check_product(K, Ns, S, activation, &p);
+  if (!flag(y_fp32)) return MOE_LORA_ERR_INVALID;
+  const int rc = check_dense(M, K, Ns, S, activation, &p);
   if (rc != MOE_LORA_OK) return rc;
-  if (M > kInt32Max || !grid_fits((M + 15) / 16, p.N)) return MOE_LORA_ERR_UNSUPPORTED;
   if (M == 0) return MOE_LORA_OK;
   if (!x || !w || !y) return MOE_LORA_ERR_INVALID;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(delta, 16) ||
@@ -99,7 +131,6 @@ int moe_lora_gemm(const uint16_t* x, const uint16_t* w, const uint16_t* bias, co
   p.residual = residual;
   p.y = y;
   p.out32 = y_fp32;
-  p.rows = p.M = M;
   return launch_gemm(p, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_LORA_OK
                                                                         : MOE_LORA_ERR_HIP;
 }
@@ -111,16 +142,10 @@ int moe_lora_moe_gemm(const uint16_t* x, int32_t x_per_pair, const uint16_t* w, 
                       int32_t K, int32_t Ns, int32_t S, int32_t E, int32_t block_m,
                       int32_t activation, uint16_t* y, void* stream) {
   ProductParams p{};
-  // the align step's own limits on M, topk, E and block_m, for one slot
-  const int64_t cap = moe_lora_align_capacity(M, topk, E, block_m);
-  if (cap < 0) return int(cap);
-  const int rc = check_product(K, Ns, S, activation, &p);
+  if (!flag(mul_routed_weight)) return MOE_LORA_ERR_INVALID;
+  const int rc = check_grouped(M, topk, K, Ns, S, E, block_m, x_per_pair, activation, &p);
   if (rc != MOE_LORA_OK) return rc;
-  if (!flag(x_per_pair) || !flag(mul_routed_weight)) return MOE_LORA_ERR_INVALID;
-  const int64_t numel = M * topk, rows = x_per_pair ? numel : M;
-  const int64_t blocks = max_total_blocks(numel, E, block_m);
-  if (rows > kMaxElements / K || !grid_fits(blocks * (block_m / 16), p.N)) return MOE_LORA_ERR_UNSUPPORTED;
-  if (numel == 0) return MOE_LORA_OK;
+  if (p.numel == 0) return MOE_LORA_OK;
   if (!x || !w || !sorted_token_ids || !expert_ids || !num_tokens_post_padded || !y ||
       (mul_routed_weight && !topk_weights))
     return MOE_LORA_ERR_INVALID;
@@ -131,20 +156,25 @@ int moe_lora_moe_gemm(const uint16_t* x, int32_t x_per_pair, const uint16_t* w, 
   p.bias = bias;
   p.delta = delta;
   p.y = y;
-  p.rows = rows;
-  p.M = M;
   p.sorted = sorted_token_ids;
   p.eids = expert_ids;
   p.ntpp = num_tokens_post_padded;
   p.wt = mul_routed_weight ? topk_weights : nullptr;
-  p.numel = int32_t(numel);
-  p.topk = topk;
-  p.E = E;
-  p.block_m = block_m;
-  p.x_per_pair = x_per_pair;
-  p.blocks = int32_t(blocks);
   return launch_moe_gemm(p, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_LORA_OK
                                                                             : MOE_LORA_ERR_HIP;
+}
+
+const char* moe_lora_gemm_kernel_name(int64_t M, int32_t K, int32_t Ns, int32_t S, int32_t activation) {
+  ProductParams p{};
+  return check_dense(M, K, Ns, S, activation, &p) == MOE_LORA_OK && M > 0 ? gemm_name(p) : nullptr;
+}
+
+const char* moe_lora_moe_gemm_kernel_name(int64_t M, int32_t topk, int32_t K, int32_t Ns, int32_t S, int32_t E,
+                                          int32_t block_m, int32_t x_per_pair, int32_t activation) {
+  ProductParams p{};
+  return check_grouped(M, topk, K, Ns, S, E, block_m, x_per_pair, activation, &p) == MOE_LORA_OK && M > 0
+             ? moe_gemm_name(p)
+             : nullptr;
 }
 
 int moe_lora_combine(const uint16_t* y, const float* topk_weights, const int32_t* topk_ids, int32_t E,

@@ -57,6 +57,9 @@ struct ProductParams {
 
 hipError_t launch_gemm(ProductParams p, hipStream_t st);      // dense
 hipError_t launch_moe_gemm(ProductParams p, hipStream_t st);  // grouped
+// The kernels they launch: name and tile.
+const char* gemm_name(const ProductParams& p);
+const char* moe_gemm_name(const ProductParams& p);
 
 // ---------------------------------------------------------------- combine
 struct CombineParams {

@@ -791,7 +791,19 @@ hipError_t rows_of(const ProductParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-}  // namespace
+// The current device's; without one, as when a kernel's name is asked for on a host
+// that has none, an MI355X's.
+int64_t compute_units() {
+  const int per = xcd_compute_units();
+  return int64_t(per > 0 ? per : 32) * kXcds;
+}
+
+// Kernels of the dense product, and their rows x columns of W.
+enum DenseForm { kRows16, kRows32, kTile32, kTile32x128, kTile64, kTile64x128, kTile128, kTile128x256, kTile256 };
+constexpr const char* kDenseNames[] = {
+    "gemm_rows_kernel 16x16", "gemm_rows_kernel 16x32", "gemm_tile_kernel 32x32",
+    "gemm_tile_kernel 32x128", "gemm_tile_kernel 64x64", "gemm_tile_kernel 64x128",
+    "gemm_tile_kernel 128x128", "gemm_tile_kernel 128x256", "gemm_tile_kernel 256x256"};
 
 // Estimates in microseconds, fitted to measured shapes with W from memory.  A tile
 // takes `block` for each 64 of K and each round over the device (one workgroup a
@@ -805,42 +817,40 @@ hipError_t rows_of(const ProductParams& p, hipStream_t st) {
 // 25.6, 16.4 and 18.7.  64 x 128, 128 x 128, 128 x 256 and 256 x 256: 512 of 4096 x 4096
 // 26, 30, 45 and 74; 1024 46, 37, 45 and 75; 2048 89, 69, 59 and 76; 4000 of 512 x 4096
 // 33, 26, 23 and 21; 4096 of 4096 x 12288 -, -, 333 and 289.
-hipError_t launch_gemm(ProductParams p, hipStream_t st) {
-  const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
+DenseForm dense_form(const ProductParams& p) {
+  const int64_t cus = compute_units();
   struct Shape {
+    DenseForm form;
     int rows, cols;
     double block, once, base;
   };
-  constexpr Shape shapes[] = {{32, 32, 0.1, 0, 3.8},    {32, 128, 0.27, 0, 2.5},  {64, 64, 0.222, 0, 2.5},
-                              {64, 128, 0.34, 0, 2.5},  {128, 128, 0.53, 0, 3.0}, {128, 256, 0.85, 1.5, 3.0},
-                              {256, 256, 1.45, 3.0, 4.0}};
-  int best = 0;
+  constexpr Shape shapes[] = {{kTile32, 32, 32, 0.1, 0, 3.8},         {kTile32x128, 32, 128, 0.27, 0, 2.5},
+                              {kTile64, 64, 64, 0.222, 0, 2.5},       {kTile64x128, 64, 128, 0.34, 0, 2.5},
+                              {kTile128, 128, 128, 0.53, 0, 3.0},     {kTile128x256, 128, 256, 0.85, 1.5, 3.0},
+                              {kTile256, 256, 256, 1.45, 3.0, 4.0}};
+  DenseForm best = kTile32;
   double least = INFINITY;
-  for (int i = 0; i < 7; ++i) {
-    const Shape& s = shapes[i];
+  for (const Shape& s : shapes) {
     const int64_t tiles = (p.M + s.rows - 1) / s.rows * column_tiles(p, s.cols);
     const double rounds = double((tiles + cus - 1) / cus), part = std::min(1.0, double(tiles) / double(cus));
     const double cost = s.base + rounds * (s.block * p.KB * (0.8 + 0.2 * part) + s.once);
-    if (cost < least) least = cost, best = i;
+    if (cost < least) least = cost, best = s.form;
   }
   if (p.M <= 16) {
     // (gated, gate and up of 16 columns)
     const int64_t grid = p.gated ? rows_grid<1, 2, false>(p) : rows_grid<1, 1, false>(p);
     const double rounds = double((grid + cus - 1) / cus);
     const double by_rows = p.gated ? 2.0 + 2.9e-3 * p.K * rounds : 1.0 + 1.8e-3 * p.K * rounds;
-    if (by_rows < least && rows_fit(grid))
-      return p.gated ? rows_of<1, 2, false>(p, st) : rows_of<1, 1, false>(p, st);
+    if (by_rows < least && rows_fit(grid)) return p.gated ? kRows32 : kRows16;
   }
-  switch (best) {
-    case 0: return tile_launch<1, 1, 2, 2, 3, false, 1, 4>(p, st);
-    case 1: return tile_launch<1, 4, 2, 2, 3, false, 2>(p, st);
-    case 2: return tile_launch<2, 2, 2, 2, 3, false, 2>(p, st);
-    case 3: return tile_launch<2, 4, 2, 2, 3, false, 2>(p, st);
-    case 4: return tile_launch<2, 4, 4, 2, 4, false>(p, st);
-    case 5: return tile_launch<2, 4, 4, 4, 3, false>(p, st);
-    default: return tile_launch<2, 4, 8, 4, 2, false>(p, st);
-  }
+  return best;
 }
+
+// Kernels of the grouped product.
+enum GroupedForm { kPairs32, kPairs64, kExperts64, kExperts128, kExperts256 };
+constexpr const char* kGroupedNames[] = {"gemm_rows_kernel 16x32", "gemm_rows_kernel 16x64",
+                                         "gemm_tile_kernel 64x256", "gemm_tile_kernel 128x256",
+                                         "gemm_tile_kernel 256x256"};
 
 // Estimates in microseconds, with the pairs spread evenly: `stream`, one expert's
 // weights at 5.5 TB/s.  The rows kernel takes 3 us, and for each piece of 16 rows
@@ -852,8 +862,8 @@ hipError_t launch_gemm(ProductParams p, hipStream_t st) {
 // 1024, 4 rows 38 and 45.  Routing that leaves most pairs to few experts is not
 // seen: the rows kernel then reads their weights once for every 16 rows, whatever
 // the tiles would take.
-hipError_t launch_moe_gemm(ProductParams p, hipStream_t st) {
-  const int64_t cus = int64_t(std::max(xcd_compute_units(), 1)) * kXcds;
+GroupedForm grouped_form(const ProductParams& p) {
+  const int64_t cus = compute_units();
   const int64_t E = p.E, used = std::min<int64_t>(p.numel, E);
   // tiles of `rows` rows
   auto tiles = [&](int rows) { return std::min<int64_t>(p.numel, std::max(used, p.numel / rows + E / 2)); };
@@ -865,8 +875,7 @@ hipError_t launch_moe_gemm(ProductParams p, hipStream_t st) {
     // 64 columns a workgroup read X half as often as 32, where that leaves a
     // workgroup for every CU (32 experts of 5760 x 2880, 2 rows each, 167.5 us and
     // 171; 8 of 512 x 1024, 96 rows 12.3 and 14.9, 8 rows 7.6 and 5.8)
-    if (tiles(16) * column_tiles(p, 64) >= cus) return rows_of<1, 4, true>(p, st);
-    return rows_of<1, 2, true>(p, st);
+    return tiles(16) * column_tiles(p, 64) >= cus ? kPairs64 : kPairs32;
   }
   // The tile whose rounds over the device cost least, the largest only with enough
   // rows to fill it whatever the routing.  (64 x 256, 128 x 256 and 256 x 256) 128
@@ -878,9 +887,37 @@ hipError_t launch_moe_gemm(ProductParams p, hipStream_t st) {
   const int64_t cols = column_tiles(p, 256);
   auto rounds = [&](int rows) { return (tiles(rows) * cols + cus - 1) / cus; };
   const int64_t cost64 = 80 * rounds(64), cost128 = 98 * rounds(128), cost256 = 140 * rounds(256);
-  if (p.block_m <= 64 && cost64 <= cost128) return tile_launch<2, 4, 2, 4, 3, true>(p, st);
-  if (p.numel <= 96 * E || cost128 <= cost256) return tile_launch<2, 4, 4, 4, 3, true>(p, st);
-  return tile_launch<2, 4, 8, 4, 2, true>(p, st);
+  if (p.block_m <= 64 && cost64 <= cost128) return kExperts64;
+  return p.numel <= 96 * E || cost128 <= cost256 ? kExperts128 : kExperts256;
+}
+
+}  // namespace
+
+const char* gemm_name(const ProductParams& p) { return kDenseNames[dense_form(p)]; }
+const char* moe_gemm_name(const ProductParams& p) { return kGroupedNames[grouped_form(p)]; }
+
+hipError_t launch_gemm(ProductParams p, hipStream_t st) {
+  switch (dense_form(p)) {
+    case kRows16: return rows_of<1, 1, false>(p, st);
+    case kRows32: return rows_of<1, 2, false>(p, st);
+    case kTile32: return tile_launch<1, 1, 2, 2, 3, false, 1, 4>(p, st);
+    case kTile32x128: return tile_launch<1, 4, 2, 2, 3, false, 2>(p, st);
+    case kTile64: return tile_launch<2, 2, 2, 2, 3, false, 2>(p, st);
+    case kTile64x128: return tile_launch<2, 4, 2, 2, 3, false, 2>(p, st);
+    case kTile128: return tile_launch<2, 4, 4, 2, 4, false>(p, st);
+    case kTile128x256: return tile_launch<2, 4, 4, 4, 3, false>(p, st);
+    default: return tile_launch<2, 4, 8, 4, 2, false>(p, st);
+  }
+}
+
+hipError_t launch_moe_gemm(ProductParams p, hipStream_t st) {
+  switch (grouped_form(p)) {
+    case kPairs32: return rows_of<1, 2, true>(p, st);
+    case kPairs64: return rows_of<1, 4, true>(p, st);
+    case kExperts64: return tile_launch<2, 4, 2, 4, 3, true>(p, st);
+    case kExperts128: return tile_launch<2, 4, 4, 4, 3, true>(p, st);
+    default: return tile_launch<2, 4, 8, 4, 2, true>(p, st);
+  }
 }
 
 }  // namespace mlr
