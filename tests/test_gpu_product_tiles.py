@@ -191,3 +191,26 @@ def test_grouped_whole_numbers_exactly(kernel, gated, size):
     want, _ = expected(x, w, ids, b, d, None, wt, False, y)
     mla.moe_lora_moe_gemm(x, w, align(ids, E, B), wt, y, mul_routed_weight=True, bias=b, delta=d)
     assert torch.equal(y.view(M * topk, -1), want.to(BF))
+
+
+@pytest.mark.parametrize("act,S,Ns,mul", [(None, 1, 72, True), (None, 2, 264, False), ("silu_mul", 2, 136, True)])
+def test_grouped_over_two_launches(act, S, Ns, mul):
+    """More align blocks than one launch of the tiles takes (16384), with an expert's run across the
+    border: the second launch's blocks, biases and weights are its own."""
+    M, topk, E, K, B = 150001, 2, 3, 72, 16
+    assert "tile" in mla.moe_gemm_kernel_name(M, topk, K, Ns, S, E, B, False, act)
+    g = gen(Ns)
+    ids = torch.randint(0, E, (M, topk), generator=g, device=DEV, dtype=torch.int32)
+    al = align(ids, E, B)
+    blocks, eids = int(al.num_tokens_post_padded[0]) // B, al.expert_ids[0]
+    assert blocks > 16384 + 1000 and int(eids[16383]) == int(eids[16384])
+    x, w, b = whole(g, M, K), whole(g, E, S, Ns, K), whole(g, E, S * Ns)
+    wt = torch.randint(1, 5, (M, topk), generator=g, device=DEV).float()
+    No = Ns if act else S * Ns
+    y = torch.full((M, topk, No), 3.0, dtype=BF, device=DEV)
+    want, err = expected(x, w, ids, b, None, act, wt if mul else None, False, y)
+    mla.moe_lora_moe_gemm(x, w, al, wt, y, mul_routed_weight=mul, bias=b, activation=act)
+    if act:
+        close(y.view(M * topk, No), want, err)
+    else:
+        assert torch.equal(y.view(M * topk, No), want.to(BF))
