@@ -628,7 +628,8 @@ MOE_LORA_API int moe_lora_gemm(const uint16_t *x, const uint16_t *w, const uint1
  * [device] x: bf16 [M, K] or [M*topk, K]; w: bf16 [E, S, Ns, K]; bias: bf16
  *          [E, S*Ns] or NULL; delta: bf16 [M, topk, S*Ns] or NULL (as
  *          fused_moe_lora with add_inputs = 0 and the same mul_routed_weight
- *          leaves it); sorted_token_ids [cap], expert_ids [cap / block_m],
+ *          leaves a zero-filled one: it does not touch rows of pairs without an
+ *          adapter, and every pair's row is read here); sorted_token_ids [cap], expert_ids [cap / block_m],
  *          num_tokens_post_padded [1]: moe_lora_align's for the same M, topk, E,
  *          block_m; topk_weights: fp32 [M, topk], may be NULL when
  *          mul_routed_weight == 0; y: bf16 [M, topk, No].  y may be delta itself

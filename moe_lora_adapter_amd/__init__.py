@@ -21,8 +21,9 @@ The bf16 base side, from the router's logits to the layer's output:
     logits = moe_lora_gemm(x, gate, out_dtype=torch.float32)
     ids, weights = moe_lora_route(logits, topk)
     moe_lora_moe_gemm(x, w13, base_align, None, h, bias=..., delta=d13, activation="silu_mul", ...)
-    moe_lora_moe_gemm(h, w2, base_align, weights, y, mul_routed_weight=True, x_per_pair=True)
-    moe_lora_combine(y, residual=x)
+    moe_lora_moe_gemm(h.view(M * topk, I), w2, base_align, weights, y, mul_routed_weight=True,
+                      x_per_pair=True)
+    moe_lora_combine(y, topk_ids=ids, E=E, residual=x)
 """
 
 from __future__ import annotations
@@ -818,7 +819,7 @@ def moe_lora_moe_gemm(x, w, align: AlignOutput, topk_weights, y, *, mul_routed_w
                       x_per_pair: bool = False, bias=None, delta=None,
                       activation: str | None = None, stream=None):
     """moe_lora_gemm with each routed pair's expert of w [E, S, Ns, K] and its bias [E, S*Ns], the
-    routed weight before delta [M, topk, S*Ns], into y [M, topk, S*Ns] ([M, topk, Ns] with a gated
+    routed weight before delta [M, topk, S*Ns] (zeros where the adapters wrote nothing), into y [M, topk, S*Ns] ([M, topk, Ns] with a gated
     activation); align is one slot's (L = 1); see moe_lora.h."""
     import torch
     bf = torch.bfloat16
