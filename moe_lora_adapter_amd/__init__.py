@@ -123,6 +123,12 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
             raise RuntimeError(
                 f"{path} is missing: build it with `python -m moe_lora_adapter_amd.build` "
                 "(or __graft_entry__.build()); there is no fallback path")
+        try:
+            # torch's HIP runtime first: loaded behind this library's, it is a second one in the
+            # process, which knows neither the other's streams nor its memory
+            import torch  # noqa: F401
+        except ImportError:
+            pass
         handle = ctypes.CDLL(path)
         for name, (res, args) in SIGNATURES.items():
             fn = getattr(handle, name)
