@@ -739,6 +739,12 @@ def _optional(t, name, dtype, shape, like, at):
     return t.data_ptr()
 
 
+def _in_32_bits(bits, where):
+    """Refuses sizes, given or-ed together, that a call's 32-bit arguments would cut short."""
+    if bits >> 31 > 0:
+        raise MoeLoraError(ERR_UNSUPPORTED, where)
+
+
 def moe_lora_route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_group: int = 1,
                    topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
                    scale: float = 1.0, topk_ids=None, topk_weights=None, stream=None):
@@ -756,6 +762,7 @@ def moe_lora_route(logits, topk: int, *, scoring: str = "softmax", bias=None, n_
     if scoring not in SCORINGS:
         raise ValueError(f"scoring must be one of {list(SCORINGS)}, got {scoring!r}")
     M, E = logits.shape
+    _in_32_bits(E | topk | n_group | topk_group | group_top, "moe_lora_route")
     at, want = logits.get_device(), (M, topk)
     pb = _optional(bias, "bias", torch.float32, (E,), logits, at)
     if topk_ids is None or topk_weights is None:
@@ -792,6 +799,7 @@ def moe_lora_gemm(x, w, y=None, *, bias=None, delta=None, activation: str | None
     if w.dim() != 3 or x.dim() != 2:
         raise ValueError("w must be [S, Ns, K] and x [M, K]")
     S, Ns, K = w.shape
+    _in_32_bits(S | Ns | K, "moe_lora_gemm")
     M, at, N = x.shape[0], w.get_device(), S * Ns
     act, gated = _activation(activation)
     No = Ns if gated else N
@@ -837,6 +845,7 @@ def moe_lora_moe_gemm(x, w, align: AlignOutput, topk_weights, y, *, mul_routed_w
     at, N = w.get_device(), S * Ns
     act, gated = _activation(activation)
     M, topk, No = y.shape
+    _in_32_bits(E | S | Ns | K | topk, "moe_lora_moe_gemm")
     if No != (Ns if gated else N):
         raise ValueError(f"y's last dim must be {Ns if gated else N}, got {No}")
     if y.dtype is not bf or not y.is_contiguous() or y.get_device() != at:
@@ -893,6 +902,8 @@ def moe_lora_combine(y, out=None, *, topk_weights=None, topk_ids=None, E: int | 
     if topk_ids is not None and E is None:
         raise ValueError("topk_ids needs E, the number of experts here")
     M, topk, N = y.shape
+    E = E or 0
+    _in_32_bits(topk | N | E, "moe_lora_combine")
     at = y.get_device()
     pw = _optional(topk_weights, "topk_weights", torch.float32, (M, topk), y, at)
     pi = _optional(topk_ids, "topk_ids", torch.int32, (M, topk), y, at)
@@ -901,7 +912,7 @@ def moe_lora_combine(y, out=None, *, topk_weights=None, topk_ids=None, E: int | 
         with _taken_on(stream):
             out = torch.empty((M, N), dtype=bf, device=y.device)
     po = _optional(out, "out", bf, (M, N), y, at)
-    args = (y.data_ptr(), pw, pi, E or 0, pr, M, topk, N, po)
+    args = (y.data_ptr(), pw, pi, E, pr, M, topk, N, po)
     raw = _direct(torch, at, stream)
     if raw is None:
         _call("moe_lora_combine", y, stream, *args)
