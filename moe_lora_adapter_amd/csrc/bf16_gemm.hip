@@ -218,7 +218,7 @@ __device__ __forceinline__ void finish_tile(const ProductParams& p, f32x4_t (&ac
 }
 
 // ---------------------------------------------------------------- few rows
-// One workgroup computes 16 MT rows x 16 NT columns of W: its kSplit wavefronts
+// One workgroup computes 16 rows x 16 NT columns of W: its kSplit wavefronts
 // take the stages w, w + kSplit, ... of K straight from memory and add their sums
 // in LDS, in order.  Bound by the stream of W: 20b-like decode w13 (64 pairs, 940
 // MB) 167 us, 5.6 TB/s, 120b-like decode w2 79 us, 6.0; more stages in flight a
@@ -227,13 +227,13 @@ __device__ __forceinline__ void finish_tile(const ProductParams& p, f32x4_t (&ac
 // groups of 16 columns are gate's and the odd ones the same of up.  Grouped, the
 // workgroups of a block take its pieces of 16 rows in steps of `step` rows.
 constexpr int kSplit = 8;
-template <int MT, int NT, bool GROUPED>
+template <int NT, bool GROUPED>
 __global__ void __launch_bounds__(kSplit * kWave) gemm_rows_kernel(ProductParams p, int ntiles, uint32_t step) {
-  __shared__ f32x4_t red[kSplit][MT * NT][kWave];
+  __shared__ f32x4_t red[kSplit][NT][kWave];
   const int tile = blockIdx.x % ntiles;
   const int lane = lane_id(), w = wave_id(), a = lane & 15, g = lane >> 4;
   const uint32_t piece = blockIdx.x / ntiles;
-  const int64_t first = int64_t(piece) * 16 * MT;  // dense: the first row
+  const int64_t first = int64_t(piece) * 16;  // dense: the first row
   int64_t e = 0;
   // grouped: the block's ids, one or two a lane, which of them are a pair's, and
   // where in the block the piece begins
@@ -244,20 +244,20 @@ __global__ void __launch_bounds__(kSplit * kWave) gemm_rows_kernel(ProductParams
   // goes to the first piece from `at` on, in this workgroup's steps, that has a pair
   auto seek = [&]() {
     for (; at < block_m; at += step)
-      if ((at < kWave ? held0 : held1) >> (at % kWave) & ((uint64_t(1) << 16 * MT) - 1)) return true;
+      if ((at < kWave ? held0 : held1) >> (at % kWave) & 0xffff) return true;
     return false;
   };
-  // row i of the piece
-  auto row_at = [&](int i) {
+  // this lane's row of the piece
+  auto row_here = [&]() {
     if constexpr (GROUPED)
-      return row_of_pair(p, uint32_t(__shfl(at < kWave ? id0 : id1, at % kWave + i)));
+      return row_of_pair(p, uint32_t(__shfl(at < kWave ? id0 : id1, at % kWave + a)));
     else
-      return row_of<false>(p, first, i);
+      return row_of<false>(p, first, a);
   };
   if constexpr (GROUPED) {
     // a block's workgroups are neighbours; what lies behind the last block comes last
-    const uint32_t parts = step / (16 * MT), block = piece / parts;
-    at = piece % parts * (16 * MT);
+    const uint32_t parts = step / 16, block = piece / parts;
+    at = piece % parts * 16;
     const int64_t start = int64_t(block) * block_m;
     const int32_t* ids = p.sorted + start;
     // (read behind the last block, too, in one wait, and not used)
@@ -295,66 +295,51 @@ __global__ void __launch_bounds__(kSplit * kWave) gemm_rows_kernel(ProductParams
     // rows of X: dense tiles are addressed from their first row, grouped ones
     // from row 0 (X is below 2 GiB there)
     const int64_t x0 = GROUPED ? 0 : first;
-    const int64_t xrows = GROUPED ? p.rows : std::min<int64_t>(p.rows - first, 16 * MT);
+    const int64_t xrows = GROUPED ? p.rows : std::min<int64_t>(p.rows - first, 16);
     const auto xr = make_rsrc(p.x + x0 * p.K, uint32_t(xrows * K2));
-    uint32_t xoff[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const RowMap r = row_at(16 * i + a);
-      xoff[i] = r.x_row >= 0 ? uint32_t((r.x_row - x0) * K2) + 16 * g : kOob;
-    }
+    const int64_t x_row = row_here().x_row;
+    const uint32_t xoff = x_row >= 0 ? uint32_t((x_row - x0) * K2) + 16 * g : kOob;
 
-    f32x4_t acc[MT][NT];
+    f32x4_t acc[NT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int f = 0; f < NT; ++f) acc[i][f] = f32x4_t{0, 0, 0, 0};
+    for (int f = 0; f < NT; ++f) acc[f] = f32x4_t{0, 0, 0, 0};
 
     for (int kb = w; kb < p.KB; kb += kSplit) {
       const uint32_t k = uint32_t(kb) * (2 * kStageK);
       const uint32_t lo = k + 16 * g < K2 ? k : kOob;
       const uint32_t hi = k + 64 + 16 * g < K2 ? k + 64 : kOob;
-      uint4 wl[NT], wh[NT], xl[MT], xh[MT];
+      uint4 wl[NT], wh[NT];
 #pragma unroll
       for (int f = 0; f < NT; ++f) {
         wl[f] = buf_ld16(wr, woff[f] + lo, 0);
         wh[f] = buf_ld16(wr, woff[f] + hi, 0);
       }
       __builtin_amdgcn_sched_barrier(0);  // the columns' loads first, a line's two halves together
+      const uint4 xl = buf_ld16(xr, xoff + lo, 0), xh = buf_ld16(xr, xoff + hi, 0);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        xl[i] = buf_ld16(xr, xoff[i] + lo, 0);
-        xh[i] = buf_ld16(xr, xoff[i] + hi, 0);
+      for (int f = 0; f < NT; ++f) {
+        acc[f] = mfma_bf16(wl[f], xl, acc[f]);
+        acc[f] = mfma_bf16(wh[f], xh, acc[f]);
       }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int f = 0; f < NT; ++f) {
-          acc[i][f] = mfma_bf16(wl[f], xl[i], acc[i][f]);
-          acc[i][f] = mfma_bf16(wh[f], xh[i], acc[i][f]);
-        }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int f = 0; f < NT; ++f) red[w][i * NT + f][lane] = acc[i][f];
+    for (int f = 0; f < NT; ++f) red[w][f][lane] = acc[f];
     __syncthreads();
     const uint16_t* bias = p.bias ? p.bias + e * p.N : nullptr;
 #pragma unroll
-    for (int t = 0; t < MT * NT; ++t) {
-      const int i = t / NT, f = t % NT;
+    for (int f = 0; f < NT; ++f) {
       // gated, the wavefront of the even group takes both
-      if (t % kSplit != w || (p.gated && (f & 1))) continue;
-      auto sum = [&](int t) {
-        f32x4_t s = red[0][t][lane];
+      if (f % kSplit != w || (p.gated && (f & 1))) continue;
+      auto sum = [&](int f) {
+        f32x4_t s = red[0][f][lane];
 #pragma unroll
-        for (int v = 1; v < kSplit; ++v) s += red[v][t][lane];
+        for (int v = 1; v < kSplit; ++v) s += red[v][f][lane];
         return s;
       };
-      const RowMap r = row_at(16 * i + a);
-      const f32x4_t s = sum(t);
+      const RowMap r = row_here();
+      const f32x4_t s = sum(f);
       f32x4_t u = {0, 0, 0, 0};
-      if (NT > 1 && p.gated) u = sum(NT > 1 ? t + 1 : t);
+      if (NT > 1 && p.gated) u = sum(NT > 1 ? f + 1 : f);
       if (r.y_row < 0 || col[f] >= p.No) continue;
       const float wt = GROUPED && p.wt ? p.wt[r.y_row] : 1.0f;
       store(p, finish(p, s, u, bias, r.y_row, col[f], wt), r.y_row, col[f]);
@@ -662,15 +647,15 @@ __global__ void __launch_bounds__(WM * WN * KG * kWave, 2)
       uint4 wf[2][2][FN], xf[2][2][FM];
       auto read = [&](const uint8_t* st, auto set, auto block) {
         each<2 * FN>([&](auto j) {
-          constexpr int h = j / FN, f = j % FN, o = block * KG * T::kBlock + 4096 * (f >> 1) + 512 * (f & 1);
+          constexpr int h = j / FN, f = j % FN, o = block * T::kBlock + 4096 * (f >> 1) + 512 * (f & 1);
           wf[set][h][f] = *reinterpret_cast<const uint4*>(st + (h ? wo ^ 64 : wo) + o);
         });
         each<2 * FM>([&](auto j) {
-          constexpr int h = j / FM, i = j % FM, o = block * KG * T::kBlock + 2048 * i;
+          constexpr int h = j / FM, i = j % FM, o = block * T::kBlock + 2048 * i;
           xf[set][h][i] = *reinterpret_cast<const uint4*>(st + (h ? xo ^ 64 : xo) + o);
         });
       };
-      static_assert(kPhases || KS % 2 == 0, "the sets take turns");
+      static_assert(KG == 1 && KS % 2 == 0, "one group of wavefronts, and the sets take turns");
       read(lds + stage * kStage, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
       for (int kb = 0; kb < stages;) {
         const int n = std::min(stages - kb, stages - lkb);
@@ -767,15 +752,14 @@ hipError_t tile_launch(ProductParams p, hipStream_t st) {
 // Pieces of an align block that start at once: as many as an expert has on
 // average, a block's workgroups take the others in turn (starting every piece
 // would leave most workgroups to find padding).
-template <int MT>
 int64_t parts_of(const ProductParams& p) {
   const int64_t each = p.numel / (int64_t(p.E) * 12) + 1;
-  return std::min<int64_t>(each, p.block_m / (16 * MT));
+  return std::min<int64_t>(each, p.block_m / 16);
 }
 
-template <int MT, int NT, bool GROUPED>
+template <int NT, bool GROUPED>
 int64_t rows_grid(const ProductParams& p) {
-  const int64_t pieces = GROUPED ? p.blocks * parts_of<MT>(p) : (p.M + 16 * MT - 1) / (16 * MT);
+  const int64_t pieces = GROUPED ? p.blocks * parts_of(p) : (p.M + 15) / 16;
   return pieces * column_tiles(p, 16 * NT);
 }
 
@@ -783,11 +767,10 @@ int64_t rows_grid(const ProductParams& p) {
 // than 2^32 threads.  (The tiles' workgroups go from tile to tile, any number.)
 bool rows_fit(int64_t grid) { return grid < (int64_t(1) << 32) / (kSplit * kWave); }
 
-template <int MT, int NT, bool GROUPED>
+template <int NT, bool GROUPED>
 hipError_t rows_of(const ProductParams& p, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_rows_kernel<MT, NT, GROUPED>), dim3(unsigned(rows_grid<MT, NT, GROUPED>(p))),
-                     dim3(kSplit * kWave), 0, st, p, column_tiles(p, 16 * NT),
-                     GROUPED ? int(parts_of<MT>(p)) * 16 * MT : 0);
+  hipLaunchKernelGGL((gemm_rows_kernel<NT, GROUPED>), dim3(unsigned(rows_grid<NT, GROUPED>(p))),
+                     dim3(kSplit * kWave), 0, st, p, column_tiles(p, 16 * NT), GROUPED ? int(parts_of(p)) * 16 : 0);
   return hipGetLastError();
 }
 
@@ -838,7 +821,7 @@ DenseForm dense_form(const ProductParams& p) {
   }
   if (p.M <= 16) {
     // (gated, gate and up of 16 columns)
-    const int64_t grid = p.gated ? rows_grid<1, 2, false>(p) : rows_grid<1, 1, false>(p);
+    const int64_t grid = p.gated ? rows_grid<2, false>(p) : rows_grid<1, false>(p);
     const double rounds = double((grid + cus - 1) / cus);
     const double by_rows = p.gated ? 2.0 + 2.9e-3 * p.K * rounds : 1.0 + 1.8e-3 * p.K * rounds;
     if (by_rows < least && rows_fit(grid)) return p.gated ? kRows32 : kRows16;
@@ -871,7 +854,7 @@ GroupedForm grouped_form(const ProductParams& p) {
   const double groups = double((p.N + 31) / 32);
   const double by_rows = 3 + double(tiles(16)) * std::max(stream, 0.004 * groups);
   const double by_tiles = 10 + std::max(0.45 * p.KB, 0.2 * p.KB + double(used) * stream);
-  if (by_rows <= by_tiles && rows_fit(rows_grid<1, 2, true>(p))) {
+  if (by_rows <= by_tiles && rows_fit(rows_grid<2, true>(p))) {
     // 64 columns a workgroup read X half as often as 32, where that leaves a
     // workgroup for every CU (32 experts of 5760 x 2880, 2 rows each, 167.5 us and
     // 171; 8 of 512 x 1024, 96 rows 12.3 and 14.9, 8 rows 7.6 and 5.8)
@@ -898,8 +881,8 @@ const char* moe_gemm_name(const ProductParams& p) { return kGroupedNames[grouped
 
 hipError_t launch_gemm(ProductParams p, hipStream_t st) {
   switch (dense_form(p)) {
-    case kRows16: return rows_of<1, 1, false>(p, st);
-    case kRows32: return rows_of<1, 2, false>(p, st);
+    case kRows16: return rows_of<1, false>(p, st);
+    case kRows32: return rows_of<2, false>(p, st);
     case kTile32: return tile_launch<1, 1, 2, 2, 3, false, 1, 4>(p, st);
     case kTile32x128: return tile_launch<1, 4, 2, 2, 3, false, 2>(p, st);
     case kTile64: return tile_launch<2, 2, 2, 2, 3, false, 2>(p, st);
@@ -912,8 +895,8 @@ hipError_t launch_gemm(ProductParams p, hipStream_t st) {
 
 hipError_t launch_moe_gemm(ProductParams p, hipStream_t st) {
   switch (grouped_form(p)) {
-    case kPairs32: return rows_of<1, 2, true>(p, st);
-    case kPairs64: return rows_of<1, 4, true>(p, st);
+    case kPairs32: return rows_of<2, true>(p, st);
+    case kPairs64: return rows_of<4, true>(p, st);
     case kExperts64: return tile_launch<2, 4, 2, 4, 3, true>(p, st);
     case kExperts128: return tile_launch<2, 4, 4, 4, 3, true>(p, st);
     default: return tile_launch<2, 4, 8, 4, 2, true>(p, st);
