@@ -29,7 +29,8 @@ def bits(t):
 
 # ---------------------------------------------------------------- dense
 
-# (M, K, Ns, S): from one row and eight columns to tiles of 256 x 256 whose last ones are short
+# (M, K, Ns, S): from one row and eight columns to many tiles of 128 x 128 whose last ones are short (sizes
+# for every kernel and tile are in product_tiles.py)
 SIZES = [(1, 8, 8, 1), (1, 2880, 264, 2), (2, 72, 2056, 2), (5, 136, 40, 1), (16, 2880, 128, 2),
          (17, 264, 104, 2), (33, 1032, 120, 1), (64, 2048, 384, 2), (100, 2880, 320, 1),
          (64, 4096, 2048, 2), (40, 520, 1032, 2), (129, 376, 136, 2), (333, 656, 520, 3),
