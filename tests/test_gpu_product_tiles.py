@@ -214,3 +214,21 @@ def test_grouped_over_two_launches(act, S, Ns, mul):
         close(y.view(M * topk, No), want, err)
     else:
         assert torch.equal(y.view(M * topk, No), want.to(BF))
+
+
+@pytest.mark.parametrize("M,Ns,S,act", [(1, 8, 1, None), (5, 136, 2, "silu_mul"), (70, 264, 1, None), (300, 504, 1, None)])
+def test_longest_k(M, Ns, S, act):
+    """K of 2^21, the most: rows of 4 MiB, and columns behind the last one at offsets towards 4 GiB.  Sums
+    of zeros and ones of either sign stay below 2^24."""
+    K = 1 << 21
+    g = gen(M)
+    x = torch.randint(-1, 2, (M, K), generator=g, device=DEV, dtype=torch.int8).to(BF)
+    w = torch.randint(-1, 2, (S, Ns, K), generator=g, device=DEV, dtype=torch.int8).to(BF)
+    y = mla.moe_lora_gemm(x, w, out_dtype=F32)
+    want = torch.zeros((M, S * Ns), dtype=D, device=DEV)
+    for k in range(0, K, 1 << 16):
+        want += x[:, k:k + (1 << 16)].to(D) @ w.view(-1, K)[:, k:k + (1 << 16)].to(D).t()
+    assert torch.equal(y, want.to(F32))
+    if act:
+        z = mla.moe_lora_gemm(x, w, activation=act, out_dtype=F32)
+        close(z, br.activate(want, act), br.activate_err(want, torch.zeros_like(want), act))
